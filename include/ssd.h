@@ -335,6 +335,121 @@ ssd_status ssd_chunk_scan_fwd_static(const ssd_shape *shape, const void *x, cons
  */
 ssd_status ssd_chunk_scan_fwd_static_status(void *stream);
 
+/*
+ * The gated delta rule: the scan's sibling whose state forgets, before it takes in a token's value,
+ * what it holds under that token's key.  (No counterpart on the pages.)  Per batch b, head h, with
+ * k_t and q_t the rows of the head's group g = h / (H/G):
+ *
+ *     S_t = exp(g_t) S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T      state P x N
+ *     o_t = scale S_t q_t
+ *
+ * or, read as steps: decay the state by exp(g_t), u = beta_t (v_t - S k_t), S += u k_t^T.
+ *
+ *   shape        as for the scan: headdim P is v's and o's width, dstate N (32, 64, 128 or 256) is
+ *                k's and q's, ngroups their rows per token; dtype is the type of q, k, v and o.
+ *   q, k         (batch, seqlen, ngroups, dstate);  v, o  (batch, seqlen, nheads, headdim)
+ *   g            (batch, seqlen, nheads) float32, the log-decay; NULL: no decay.
+ *   beta         (batch, seqlen, nheads) float32.
+ *   options      required.  qk_l2norm = 1: q_t and k_t are first divided by
+ *                sqrt(sum of their squares + 1e-6).  Without it the keys should be of norm 1 (or
+ *                beta |k|^2 below 2): past that the recurrence grows from token to token.
+ *   init_state, final_state
+ *                (batch, nheads, headdim, dstate) float32, both nullable (zeros; not written).
+ *                final_state may be init_state.  o must not alias any input.
+ *   workspace    ssd_delta_rule_workspace_size bytes (0: invalid shape), 256-byte aligned, with
+ *                the scan's rules: contents do not matter, concurrent calls use distinct ones.
+ * q, k, v, o and the states must be 16-byte aligned.  batch == 0 or seqlen == 0 is valid.
+ */
+typedef struct {
+    float scale;          /* of the output; usually 1 / sqrt(dstate) */
+    int32_t qk_l2norm;    /* 0 or 1 */
+} ssd_delta_options;
+
+size_t ssd_delta_rule_workspace_size(const ssd_shape *shape);
+ssd_status ssd_delta_rule_fwd(const ssd_shape *shape, const void *q, const void *k,
+                              const void *v, const float *g, const float *beta,
+                              const ssd_delta_options *options, const float *init_state, void *o,
+                              float *final_state, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/*
+ * The same over packed sequences, as ssd_chunk_scan_varlen_fwd packs them: batch 1, sequence s is
+ * tokens cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (any length, 0 included) with its own state
+ * init_states[s] (nullable: zeros) and final_states[s] (nullable).  An inconsistent cu_seqlens
+ * computes nothing, and ssd_workspace_status() then returns SSD_ERR_INVALID_ARG.
+ */
+size_t ssd_delta_rule_varlen_workspace_size(const ssd_shape *shape, int nseq);
+ssd_status ssd_delta_rule_varlen_fwd(const ssd_shape *shape, const void *q, const void *k,
+                                     const void *v, const float *g, const float *beta,
+                                     const ssd_delta_options *options, const int32_t *cu_seqlens,
+                                     int nseq, const float *init_states, void *o,
+                                     float *final_states, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
+/*
+ * One token per sequence (decode): state (batch, nheads, headdim, dstate) float32 is updated in
+ * place; q, k (batch, ngroups, dstate), v, o (batch, nheads, headdim), g (nullable) and beta
+ * (batch, nheads).  shape->seqlen is ignored.  state, q and k must be 16-byte aligned.
+ */
+ssd_status ssd_delta_rule_update(const ssd_shape *shape, float *state, const void *q,
+                                 const void *k, const void *v, const float *g,
+                                 const float *beta, const ssd_delta_options *options, void *o,
+                                 void *stream);
+
+/*
+ * Root-mean-square norm of the block's rows.  (No counterpart on the pages: the norm in front of a
+ * mixer's input projection, and the gated one in front of its output projection.)
+ *
+ *     h = x + residual                      rounded to `dtype`; or x (no residual)
+ *     y = h / sqrt(mean(h^2) + eps) * weight
+ *
+ *   gate         SSD_GATE_PRE: h = x silu(z) is normalised; SSD_GATE_POST: y is multiplied by
+ *                silu(z).  z goes with a gate; a gate and a residual cannot be combined.
+ *   x, residual, z, residual_out
+ *                (rows, dim) contiguous, element type `dtype`.  residual_out receives h and goes
+ *                with residual; it may be residual or x itself.
+ *   weight       (dim) float32.
+ *   quant_group  0: y is (rows, dim) of `dtype` (it may be x itself).  dim, or 32, 64 or 128
+ *                dividing dim: y is (rows, dim) e4m3 bytes and scales (rows, dim / quant_group)
+ *                float32, scale = max(largest |y| of the group / 448, 1e-30), and y / scale is
+ *                rounded to nearest.  A NaN in a group makes its scale NaN.
+ *
+ * dim is 1..16384.  Rows of whole 16-byte vectors (dim a multiple of 8 in bf16, of 4 in float32)
+ * need 16-byte aligned pointers (weight and y included), others are aligned to their elements.
+ * Sums are float32.  Nothing is allocated; rows == 0 is a no-op.
+ */
+typedef enum { SSD_GATE_NONE = 0, SSD_GATE_PRE = 1, SSD_GATE_POST = 2 } ssd_gate;
+
+typedef struct {
+    int64_t rows;          /* >= 0 */
+    int64_t dim;           /* 1..16384 */
+    int32_t dtype;         /* ssd_dtype of x, residual, z, y and of their gradients */
+    int32_t gate;          /* ssd_gate */
+    int32_t quant_group;   /* 0, dim, or 32, 64 or 128 dividing dim */
+    float eps;             /* >= 0 */
+} ssd_norm_desc;
+
+ssd_status ssd_rms_norm(const ssd_norm_desc *desc, const void *x, const void *residual,
+                        const void *z, const float *weight, void *y, float *scales,
+                        void *residual_out, void *stream);
+
+/*
+ * Gradients of ssd_rms_norm with respect to x (and the residual, which has the same), z and
+ * weight, given dy.  x is the forward's input, or its residual_out where it had a residual.
+ *
+ *   dresidual    nullable: the gradient that reaches residual_out from elsewhere, added to dx.
+ *   dx, dz       (rows, dim) of `dtype`; dz goes with a gate.  dx may be dy or dresidual itself.
+ *   dweight      (dim) float32, summed over the rows in a fixed order: repeated calls give the
+ *                same bits.
+ *   workspace    ssd_rms_norm_bwd_workspace_size bytes (0: invalid arguments), 256-byte aligned.
+ * desc->quant_group must be 0.
+ */
+size_t ssd_rms_norm_bwd_workspace_size(const ssd_norm_desc *desc);
+ssd_status ssd_rms_norm_bwd(const ssd_norm_desc *desc, const void *x, const void *z,
+                            const float *weight, const void *dy, const void *dresidual, void *dx,
+                            void *dz, float *dweight, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
 /* Message for the calling thread's last non-OK status ("" if none). */
 const char *ssd_last_error(void);
 

@@ -1,0 +1,211 @@
+// C ABI entry points of the gated delta rule (include/ssd.h): argument validation, workspace
+// carving and the choice of the kernels.
+#include "api.cuh"
+#include "delta.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int kTableChunk = 32;   // tokens per entry of the chunk table
+
+ssd_status check_delta(const ssd_shape *s, const ssd_delta_options *o, bool need_seq)
+{
+    ssd_status st = api_check_shape(s, need_seq);
+    if (st != SSD_OK) return st;
+    if (!delta_recurrent_supported((int)s->dstate))
+        return api_fail(SSD_ERR_UNSUPPORTED, "the delta rule needs dstate 32, 64, 128 or 256 "
+                        "(got %lld)", (long long)s->dstate);
+    if (o && o->qk_l2norm != 0 && o->qk_l2norm != 1)
+        return api_fail(SSD_ERR_INVALID_ARG, "qk_l2norm must be 0 or 1");
+    const int64_t blocks = (s->headdim + 31) / 32;
+    if (s->batch * s->nheads * blocks > 0x7fffffffLL)
+        return api_fail(SSD_ERR_UNSUPPORTED, "problem too large for one launch grid");
+    return SSD_OK;
+}
+
+DeltaArgs delta_args(const ssd_shape *s, const ssd_delta_options *o, const void *q,
+                     const void *k, const void *v, const float *g, const float *beta)
+{
+    DeltaArgs a = {};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.g = g;
+    a.beta = beta;
+    a.batch = s->batch;
+    a.L = s->seqlen;
+    a.H = (int)s->nheads;
+    a.G = (int)s->ngroups;
+    a.P = (int)s->headdim;
+    a.N = (int)s->dstate;
+    a.scale = o->scale;
+    a.l2norm = o->qk_l2norm;
+    return a;
+}
+
+struct VarlenWs {
+    size_t status, tab, cstart, total;
+    int64_t slots;
+};
+
+VarlenWs varlen_ws(const ssd_shape *s, int nseq)
+{
+    VarlenWs w;
+    w.slots = s->seqlen / kTableChunk + nseq;
+    w.status = 0;
+    w.tab = 256;
+    w.cstart = w.tab + api_round256((size_t)w.slots * sizeof(int2));
+    w.total = w.cstart + api_round256((size_t)(nseq + 1) * sizeof(int32_t));
+    return w;
+}
+
+ssd_status check_delta_varlen(const ssd_shape *s, int nseq, const ssd_delta_options *o)
+{
+    ssd_status st = check_delta(s, o, true);
+    if (st != SSD_OK) return st;
+    if (s->batch != 1)
+        return api_fail(SSD_ERR_INVALID_ARG, "variable-length input is packed: batch must be 1 "
+                        "(got %lld)", (long long)s->batch);
+    if (nseq < 1) return api_fail(SSD_ERR_INVALID_ARG, "nseq must be >= 1 (got %d)", nseq);
+    if (s->seqlen > 0x7fffffffLL - 256)
+        return api_fail(SSD_ERR_UNSUPPORTED, "packed token count must fit int32 cu_seqlens");
+    if ((int64_t)nseq * s->nheads * 4 > 0x7fffffffLL)
+        return api_fail(SSD_ERR_UNSUPPORTED, "problem too large for one launch grid");
+    return SSD_OK;
+}
+
+ssd_status check_pointers(const DeltaArgs &a, const void *workspace)
+{
+    if (!a.q || !a.k || !a.v || !a.beta || !a.o || !workspace)
+        return api_fail(SSD_ERR_INVALID_ARG,
+                        "q, k, v, beta, o and workspace must be non-NULL");
+    if (!api_aligned(a.q, 16) || !api_aligned(a.k, 16) || !api_aligned(a.v, 16) ||
+        !api_aligned(a.o, 16))
+        return api_fail(SSD_ERR_INVALID_ARG, "q, k, v and o must be 16-byte aligned");
+    if (!api_aligned(workspace, 256))
+        return api_fail(SSD_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    return SSD_OK;
+}
+
+ssd_status check_states(const float *init, const float *final_state)
+{
+    if (!api_aligned(init, 16) || !api_aligned(final_state, 16))
+        return api_fail(SSD_ERR_INVALID_ARG, "initial and final states must be 16-byte aligned");
+    return SSD_OK;
+}
+
+}  // namespace
+}  // namespace ssd
+
+using namespace ssd;
+
+extern "C" {
+
+size_t ssd_delta_rule_workspace_size(const ssd_shape *shape)
+{
+    if (check_delta(shape, nullptr, true) != SSD_OK) return 0;
+    return 256;
+}
+
+ssd_status ssd_delta_rule_fwd(const ssd_shape *shape, const void *q, const void *k,
+                              const void *v, const float *g, const float *beta,
+                              const ssd_delta_options *options, const float *init_state, void *o,
+                              float *final_state, void *workspace, size_t workspace_bytes,
+                              void *stream)
+{
+    if (!options) return api_fail(SSD_ERR_INVALID_ARG, "options is NULL");
+    ssd_status st = check_delta(shape, options, true);
+    if (st == SSD_OK) st = check_states(init_state, final_state);
+    if (st != SSD_OK) return st;
+    const ssd_shape s = *shape;
+    cudaStream_t cst = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (s.batch == 0) return SSD_OK;
+    if (s.seqlen == 0) {
+        if (!final_state) return SSD_OK;
+        e = launch_fill_final(init_state, final_state,
+                              s.batch * s.nheads * s.headdim * s.dstate, cst);
+        return e == cudaSuccess ? SSD_OK : api_cuda_fail(e, "fill final state");
+    }
+    DeltaArgs a = delta_args(&s, options, q, k, v, g, beta);
+    a.init = init_state;
+    a.o = o;
+    a.final_state = final_state;
+    st = check_pointers(a, workspace);
+    if (st != SSD_OK) return st;
+    const size_t need = ssd_delta_rule_workspace_size(shape);
+    if (workspace_bytes < need)
+        return api_fail(SSD_ERR_INVALID_ARG, "workspace too small: need %zu bytes, got %zu", need,
+                        workspace_bytes);
+    e = launch_delta_recurrent(a, s.dtype == SSD_BF16, nullptr, cst);
+    return e == cudaSuccess ? SSD_OK : api_cuda_fail(e, "delta rule launch");
+}
+
+size_t ssd_delta_rule_varlen_workspace_size(const ssd_shape *shape, int nseq)
+{
+    if (check_delta_varlen(shape, nseq, nullptr) != SSD_OK) return 0;
+    return varlen_ws(shape, nseq).total;
+}
+
+ssd_status ssd_delta_rule_varlen_fwd(const ssd_shape *shape, const void *q, const void *k,
+                                     const void *v, const float *g, const float *beta,
+                                     const ssd_delta_options *options, const int32_t *cu_seqlens,
+                                     int nseq, const float *init_states, void *o,
+                                     float *final_states, void *workspace,
+                                     size_t workspace_bytes, void *stream)
+{
+    if (!options) return api_fail(SSD_ERR_INVALID_ARG, "options is NULL");
+    ssd_status st = check_delta_varlen(shape, nseq, options);
+    if (st == SSD_OK) st = check_states(init_states, final_states);
+    if (st != SSD_OK) return st;
+    if (!cu_seqlens) return api_fail(SSD_ERR_INVALID_ARG, "cu_seqlens must be non-NULL");
+    DeltaArgs a = delta_args(shape, options, q, k, v, g, beta);
+    a.init = init_states;
+    a.o = o;
+    a.final_state = final_states;
+    a.cu = cu_seqlens;
+    a.nseq = nseq;
+    if (a.L > 0) {
+        st = check_pointers(a, workspace);
+        if (st != SSD_OK) return st;
+    }
+    const VarlenWs w = varlen_ws(shape, nseq);
+    if (!workspace || !api_aligned(workspace, 256) || workspace_bytes < w.total)
+        return api_fail(SSD_ERR_INVALID_ARG, "workspace too small or unaligned: need %zu bytes, "
+                        "got %zu", w.total, workspace_bytes);
+    cudaStream_t cst = static_cast<cudaStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    int *status = reinterpret_cast<int *>(ws + w.status);
+    cudaError_t e = launch_build_chunk_table(
+        cu_seqlens, nseq, a.L, kTableChunk, w.slots, reinterpret_cast<int2 *>(ws + w.tab),
+        reinterpret_cast<int32_t *>(ws + w.cstart), status, cst);
+    if (e == cudaSuccess)
+        e = launch_delta_recurrent(a, shape->dtype == SSD_BF16, status, cst);
+    return e == cudaSuccess ? SSD_OK : api_cuda_fail(e, "delta rule launch");
+}
+
+ssd_status ssd_delta_rule_update(const ssd_shape *shape, float *state, const void *q,
+                                 const void *k, const void *v, const float *g,
+                                 const float *beta, const ssd_delta_options *options, void *o,
+                                 void *stream)
+{
+    if (!options) return api_fail(SSD_ERR_INVALID_ARG, "options is NULL");
+    ssd_status st = check_delta(shape, options, false);
+    if (st != SSD_OK) return st;
+    if (shape->batch == 0) return SSD_OK;
+    ssd_shape s = *shape;
+    s.seqlen = 1;
+    DeltaArgs a = delta_args(&s, options, q, k, v, g, beta);
+    a.init = state;
+    a.final_state = state;
+    a.o = o;
+    if (!state || !q || !k || !v || !beta || !o)
+        return api_fail(SSD_ERR_INVALID_ARG, "state, q, k, v, beta and o must be non-NULL");
+    if (!api_aligned(state, 16) || !api_aligned(q, 16) || !api_aligned(k, 16))
+        return api_fail(SSD_ERR_INVALID_ARG, "state, q and k must be 16-byte aligned");
+    cudaError_t e = launch_delta_recurrent(a, s.dtype == SSD_BF16, nullptr,
+                                           static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SSD_OK : api_cuda_fail(e, "delta rule update launch");
+}
+
+}  // extern "C"

@@ -17,6 +17,7 @@
 
 #include "../../include/ssd.h"
 #include "../../include/ssd_testing.h"
+#include "api.cuh"
 #include "common.cuh"
 
 namespace {
@@ -133,6 +134,20 @@ ssd_status check_varlen(const ssd_shape *s, int nseq, int Q)
 }  // namespace
 
 void ssd::set_last_error(const char *msg) { snprintf(g_err, sizeof(g_err), "%s", msg); }
+
+ssd_status ssd::api_fail(ssd_status s, const char *fmt, ...)
+{
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof(g_err), fmt, ap);
+    va_end(ap);
+    return s;
+}
+ssd_status ssd::api_cuda_fail(cudaError_t e, const char *what) { return cuda_fail(e, what); }
+ssd_status ssd::api_check_shape(const ssd_shape *s, bool need_seq)
+{
+    return check_shape(s, need_seq);
+}
 
 namespace {
 std::atomic<int> g_test_kernel{0};

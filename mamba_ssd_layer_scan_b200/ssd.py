@@ -7,6 +7,16 @@ without the CUDA kernels, loading it raises.
     y, final = chunk_scan_fwd(x, dt, A, B, C, D, chunk_size=256, init_state=None)
     y, finals = chunk_scan_varlen_fwd(x, dt, A, B, C, D, cu_seqlens)   # packed sequences
     y = state_update(state, x, dt, A, B, C, D)          # state updated in place
+
+The gated delta rule, the same kinds of call with keys, queries and values, and the norm that
+stands in front of and behind either mixer:
+
+    o, final = delta_rule_fwd(q, k, v, g, beta, qk_l2norm=True)
+    o, finals = delta_rule_varlen_fwd(q, k, v, g, beta, cu_seqlens)
+    o = delta_rule_update(state, q, k, v, g, beta)      # one token, state updated in place
+    y, h = rms_norm(x, weight, residual=residual)
+    y8, scales = rms_norm(x, weight, z=z, gate="pre", quant_group=128)
+    grads = rms_norm_bwd(x, weight, dy)
 """
 from __future__ import annotations
 
@@ -40,6 +50,19 @@ class FwdOptions(ctypes.Structure):
     _fields_ = [("z", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p),
                 ("dt_softplus", ctypes.c_int32), ("dt_min", ctypes.c_float),
                 ("dt_max", ctypes.c_float)]
+
+
+class DeltaOptions(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("qk_l2norm", ctypes.c_int32)]
+
+
+GATES = {"none": 0, "pre": 1, "post": 2}
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("gate", ctypes.c_int32), ("quant_group", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -103,6 +126,28 @@ def lib():
                                    _vp, _vp]
     L.ssd_state_update_ex.restype = ctypes.c_int
     L.ssd_state_update_ex.argtypes = L.ssd_state_update.argtypes + [ctypes.POINTER(FwdOptions)]
+    L.ssd_delta_rule_workspace_size.restype = ctypes.c_size_t
+    L.ssd_delta_rule_workspace_size.argtypes = [ctypes.POINTER(Shape)]
+    L.ssd_delta_rule_fwd.restype = ctypes.c_int
+    L.ssd_delta_rule_fwd.argtypes = [ctypes.POINTER(Shape), _vp, _vp, _vp, _vp, _vp,
+                                     ctypes.POINTER(DeltaOptions), _vp, _vp, _vp, _vp,
+                                     ctypes.c_size_t, _vp]
+    L.ssd_delta_rule_varlen_workspace_size.restype = ctypes.c_size_t
+    L.ssd_delta_rule_varlen_workspace_size.argtypes = [ctypes.POINTER(Shape), ctypes.c_int]
+    L.ssd_delta_rule_varlen_fwd.restype = ctypes.c_int
+    L.ssd_delta_rule_varlen_fwd.argtypes = [ctypes.POINTER(Shape), _vp, _vp, _vp, _vp, _vp,
+                                            ctypes.POINTER(DeltaOptions), _vp, ctypes.c_int, _vp,
+                                            _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    L.ssd_delta_rule_update.restype = ctypes.c_int
+    L.ssd_delta_rule_update.argtypes = [ctypes.POINTER(Shape), _vp, _vp, _vp, _vp, _vp, _vp,
+                                        ctypes.POINTER(DeltaOptions), _vp, _vp]
+    L.ssd_rms_norm.restype = ctypes.c_int
+    L.ssd_rms_norm.argtypes = [ctypes.POINTER(NormDesc), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+    L.ssd_rms_norm_bwd_workspace_size.restype = ctypes.c_size_t
+    L.ssd_rms_norm_bwd_workspace_size.argtypes = [ctypes.POINTER(NormDesc)]
+    L.ssd_rms_norm_bwd.restype = ctypes.c_int
+    L.ssd_rms_norm_bwd.argtypes = [ctypes.POINTER(NormDesc), _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                   _vp, _vp, ctypes.c_size_t, _vp]
     L.ssd_workspace_status.restype = ctypes.c_int
     L.ssd_workspace_status.argtypes = [_vp, ctypes.c_size_t, _vp]
     L.ssd_last_error.restype = ctypes.c_char_p
@@ -483,6 +528,229 @@ def state_update(state, x, dt, A, B, C, D, y=None, stream=None, z=None, dt_bias=
         opts = FwdOptions(_ptr(z), _ptr(dt_bias), 1 if dt_softplus else 0, lo, hi)
         _check(lib().ssd_state_update_ex(*args, ctypes.byref(opts)))
     return y
+
+
+# ---------------------------------------------------------------- gated delta rule
+def _on(t, name, shape, dtype, device):
+    """Refuse what the kernels would misread: another shape, type, device, or strides."""
+    _require(t, name, dtype, device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+class _Call:
+    """A call's device and stream (the device's current stream by default): allocates outputs and
+    workspaces, and keeps their memory from being handed out again while that stream uses it."""
+
+    def __init__(self, x, stream):
+        torch = _torch()
+        if not x.is_cuda:
+            raise ValueError(f"tensors must be on a CUDA device, got {x.device}")
+        self.device = x.device
+        self.own = torch.cuda.current_stream(x.device)
+        self.stream = self.own if stream is None else stream
+        if self.stream.device != x.device:
+            raise ValueError(f"the stream is on {self.stream.device}, the tensors on {x.device}")
+
+    def empty(self, shape, dtype):
+        torch = _torch()
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self.stream != self.own:
+            t.record_stream(self.stream)
+        return t
+
+    def workspace(self, given, size):
+        torch = _torch()
+        if given is None:
+            return self.empty(size, torch.uint8)
+        _require(given, "workspace", torch.uint8, self.device)
+        return given
+
+    def run(self, function, *args):
+        torch = _torch()
+        with torch.cuda.device(self.device):
+            _check(function(*args, self.stream.cuda_stream))
+
+
+def _delta_inputs(q, k, v, g, beta, state_rows, states, seq=True):
+    """Shape of the call after every tensor has been checked against q, k and v."""
+    torch = _torch()
+    if v.dim() != (4 if seq else 3) or q.dim() != v.dim():
+        raise ValueError("q, k and v must be (batch, seqlen, heads, width)" if seq else
+                         "q, k and v must be (batch, heads, width)")
+    lead, (H, P), (G, N) = tuple(v.shape[:-2]), v.shape[-2:], q.shape[-2:]
+    code = _dtype_code(v)
+    _on(v, "v", v.shape, v.dtype, v.device)
+    for t, n in ((q, "q"), (k, "k")):
+        _on(t, n, lead + (G, N), v.dtype, v.device)
+    if g is not None:
+        _on(g, "g", lead + (H,), torch.float32, v.device)
+    _on(beta, "beta", lead + (H,), torch.float32, v.device)
+    rows = lead[0] if state_rows is None else state_rows
+    for t, n in states:
+        if t is not None:
+            _on(t, n, (rows, H, P, N), torch.float32, v.device)
+    return make_shape(lead[0], lead[1] if seq else 1, H, P, N, G, code)
+
+
+def _delta_options(scale, dstate, qk_l2norm) -> DeltaOptions:
+    return DeltaOptions(dstate ** -0.5 if scale is None else scale, 1 if qk_l2norm else 0)
+
+
+def delta_rule_workspace_size(shape: Shape) -> int:
+    n = lib().ssd_delta_rule_workspace_size(ctypes.byref(shape))
+    if n == 0:
+        raise SSDError(SSD_ERR_INVALID_ARG, last_error())
+    return n
+
+
+def delta_rule_fwd(q, k, v, g, beta, scale=None, init_state=None, qk_l2norm: bool = False,
+                   return_final_state: bool = True, o=None, final_state=None, workspace=None,
+                   stream=None):
+    """The gated delta rule over whole sequences (ssd_delta_rule_fwd).  q, k (b, L, G, N) and v
+    (b, L, H, P) float32 or bf16, g (b, L, H) float32 log-decay or None, beta (b, L, H) float32,
+    init_state (b, H, P, N) float32 or None; scale defaults to N ** -0.5.  Returns
+    (o, final_state or None)."""
+    torch = _torch()
+    shape = _delta_inputs(q, k, v, g, beta, None,
+                          ((init_state, "init_state"), (final_state, "final_state")))
+    call = _Call(v, stream)
+    if o is None:
+        o = call.empty(v.shape, v.dtype)
+    _on(o, "o", v.shape, v.dtype, v.device)
+    if final_state is None and return_final_state:
+        final_state = call.empty((shape.batch, shape.nheads, shape.headdim, shape.dstate),
+                                 torch.float32)
+    workspace = call.workspace(workspace, delta_rule_workspace_size(shape))
+    call.run(lib().ssd_delta_rule_fwd, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+             _ptr(beta), ctypes.byref(_delta_options(scale, shape.dstate, qk_l2norm)),
+             _ptr(init_state), _ptr(o), _ptr(final_state), _ptr(workspace), workspace.numel())
+    return o, final_state
+
+
+def delta_rule_varlen_fwd(q, k, v, g, beta, cu_seqlens, scale=None, init_states=None,
+                          qk_l2norm: bool = False, return_final_states: bool = True, o=None,
+                          final_states=None, workspace=None, stream=None):
+    """The gated delta rule over packed sequences (ssd_delta_rule_varlen_fwd): tensors as for
+    delta_rule_fwd with batch 1, cu_seqlens (nseq + 1,) int32 on the device, states (nseq, H, P, N).
+    Returns (o, final_states or None)."""
+    torch = _torch()
+    nseq = cu_seqlens.numel() - 1
+    shape = _delta_inputs(q, k, v, g, beta, nseq,
+                          ((init_states, "init_states"), (final_states, "final_states")))
+    _on(cu_seqlens, "cu_seqlens", (nseq + 1,), torch.int32, v.device)
+    call = _Call(v, stream)
+    if o is None:
+        o = call.empty(v.shape, v.dtype)
+    _on(o, "o", v.shape, v.dtype, v.device)
+    n = lib().ssd_delta_rule_varlen_workspace_size(ctypes.byref(shape), nseq)
+    if n == 0:
+        raise SSDError(SSD_ERR_INVALID_ARG, last_error())
+    if final_states is None and return_final_states:
+        final_states = call.empty((nseq, shape.nheads, shape.headdim, shape.dstate),
+                                  torch.float32)
+    workspace = call.workspace(workspace, n)
+    call.run(lib().ssd_delta_rule_varlen_fwd, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v),
+             _ptr(g), _ptr(beta),
+             ctypes.byref(_delta_options(scale, shape.dstate, qk_l2norm)), _ptr(cu_seqlens), nseq,
+             _ptr(init_states), _ptr(o), _ptr(final_states), _ptr(workspace), workspace.numel())
+    return o, final_states
+
+
+def delta_rule_update(state, q, k, v, g, beta, scale=None, qk_l2norm: bool = False, o=None,
+                      stream=None):
+    """One token per sequence (ssd_delta_rule_update).  state (b, H, P, N) float32 (in place),
+    q, k (b, G, N), v (b, H, P), g (b, H) float32 or None, beta (b, H) float32.  Returns
+    o (b, H, P)."""
+    shape = _delta_inputs(q, k, v, g, beta, None, ((state, "state"),), seq=False)
+    call = _Call(v, stream)
+    if o is None:
+        o = call.empty(v.shape, v.dtype)
+    _on(o, "o", v.shape, v.dtype, v.device)
+    call.run(lib().ssd_delta_rule_update, ctypes.byref(shape), _ptr(state), _ptr(q), _ptr(k),
+             _ptr(v), _ptr(g), _ptr(beta),
+             ctypes.byref(_delta_options(scale, shape.dstate, qk_l2norm)), _ptr(o))
+    return o
+
+
+# ---------------------------------------------------------------- RMS norm
+def _norm_desc(x, weight, eps, z, gate, quant_group, others) -> NormDesc:
+    """The call's description after every tensor has been checked against x."""
+    torch = _torch()
+    if gate not in GATES:
+        raise ValueError(f"gate must be one of {sorted(GATES)}, got {gate!r}")
+    if (gate != "none") != (z is not None):
+        raise ValueError("z goes with a gate, and a gate with z")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"x must be (..., dim), got {tuple(x.shape)}")
+    dim = x.shape[-1]
+    if quant_group and (quant_group < 0 or dim % quant_group):
+        raise ValueError(f"quant_group must divide dim {dim}, got {quant_group}")
+    code = _dtype_code(x)
+    for t, n in ((x, "x"), (z, "z")) + others:
+        if t is not None:
+            _on(t, n, x.shape, x.dtype, x.device)
+    _on(weight, "weight", (dim,), torch.float32, x.device)
+    return NormDesc(x.numel() // dim, dim, code, GATES[gate], quant_group, eps)
+
+
+def rms_norm(x, weight, eps: float = 1e-5, residual=None, z=None, gate: str = "none",
+             quant_group: int = 0, y=None, scales=None, residual_out=None, stream=None):
+    """RMS norm over the last dimension of x (..., dim) float32 or bf16, weight (dim,) float32
+    (ssd_rms_norm).  residual: x + residual is normalised, and returned as residual_out.  z with
+    gate "pre" (x * silu(z) is normalised) or "post" (the normalised is multiplied by silu(z)).
+    quant_group: y in float8_e4m3fn with one float32 scale per quant_group elements (dim: per
+    row).  Returns y, followed by the scales (..., dim // quant_group) if quantised and by
+    residual_out if there is a residual; y alone where neither is."""
+    torch = _torch()
+    desc = _norm_desc(x, weight, eps, z, gate, quant_group,
+                      ((residual, "residual"), (residual_out, "residual_out")))
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out goes with residual")
+    call = _Call(x, stream)
+    out_dtype = torch.float8_e4m3fn if quant_group else x.dtype
+    if y is None:
+        y = call.empty(x.shape, out_dtype)
+    _on(y, "y", x.shape, out_dtype, x.device)
+    if quant_group:
+        shape = tuple(x.shape[:-1]) + (x.shape[-1] // quant_group,)
+        if scales is None:
+            scales = call.empty(shape, torch.float32)
+        _on(scales, "scales", shape, torch.float32, x.device)
+    elif scales is not None:
+        raise ValueError("scales go with quant_group")
+    if residual is not None and residual_out is None:
+        residual_out = call.empty(x.shape, x.dtype)
+    call.run(lib().ssd_rms_norm, ctypes.byref(desc), _ptr(x), _ptr(residual), _ptr(z),
+             _ptr(weight), _ptr(y), _ptr(scales), _ptr(residual_out))
+    out = [t for t in (y, scales, residual_out) if t is not None]
+    return out[0] if len(out) == 1 else tuple(out)
+
+
+def rms_norm_bwd(x, weight, dy, eps: float = 1e-5, z=None, gate: str = "none", dresidual=None,
+                 dx=None, dz=None, workspace=None, stream=None):
+    """Gradients of rms_norm (ssd_rms_norm_bwd): x is the forward's input, or its residual_out
+    where it had a residual; dresidual is the gradient that reaches residual_out from elsewhere
+    (added to dx).  Returns a dict of dx (the residual's gradient too), dweight (float32) and, with
+    a gate, dz."""
+    torch = _torch()
+    desc = _norm_desc(x, weight, eps, z, gate, 0, ((dy, "dy"), (dresidual, "dresidual"),
+                                                   (dx, "dx"), (dz, "dz")))
+    if z is None and dz is not None:
+        raise ValueError("dz goes with z")
+    call = _Call(x, stream)
+    g = dict(dx=call.empty(x.shape, x.dtype) if dx is None else dx,
+             dweight=call.empty(weight.shape, torch.float32))
+    if z is not None:
+        g["dz"] = call.empty(x.shape, x.dtype) if dz is None else dz
+    n = lib().ssd_rms_norm_bwd_workspace_size(ctypes.byref(desc))
+    if n == 0:
+        raise SSDError(SSD_ERR_INVALID_ARG, last_error())
+    workspace = call.workspace(workspace, n)
+    call.run(lib().ssd_rms_norm_bwd, ctypes.byref(desc), _ptr(x), _ptr(z), _ptr(weight), _ptr(dy),
+             _ptr(dresidual), _ptr(g["dx"]), _ptr(g.get("dz")), _ptr(g["dweight"]),
+             _ptr(workspace), workspace.numel())
+    return g
 
 
 def workspace_status(workspace, stream=None) -> int:
