@@ -27,4 +27,28 @@ bool delta_recurrent_supported(int N);
 cudaError_t launch_delta_recurrent(const DeltaArgs &a, bool is_bf16, const int *status,
                                    cudaStream_t st);
 
+// The chunked form: chunks of kDeltaChunk tokens on warp-level bf16 matrix instructions (bf16
+// inputs, N 64 or 128, P a multiple of 16).
+constexpr int kDeltaChunk = 32;
+bool delta_chunk_supported(bool is_bf16, int P, int N);
+
+// What delta_prep_kernel leaves of one chunk of one head, 6.5 KB in the workspace (8.5 KB with the
+// second part of att, for the backward).  Row-major 32 x 32 bf16 triangles in two parts each.
+struct DeltaItem {
+    static constexpr int kTri = kDeltaChunk * kDeltaChunk * 2;   // bytes of one part
+    static constexpr int kInvHi = 0, kInvLo = kTri, kVec = 2 * kTri;
+    static constexpr int kAttHi = kVec + 512, kAttLo = kAttHi + kTri;
+    // floats at kVec: ek[32], sw[32], eq[32], the chunk's decay
+    static __host__ __device__ constexpr int bytes(bool two_parts)
+    {
+        return two_parts ? kAttLo + kTri : kAttLo;
+    }
+};
+
+cudaError_t launch_delta_prep(const DeltaArgs &a, char *items, bool for_backward, int64_t nchunks,
+                              const int2 *tab, cudaStream_t st);
+cudaError_t launch_delta_chain(const DeltaArgs &a, const char *items, int64_t nchunks,
+                               const int2 *tab, const int32_t *cstart, const int *status,
+                               cudaStream_t st);
+
 }  // namespace ssd

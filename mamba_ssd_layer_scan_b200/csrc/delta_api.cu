@@ -6,7 +6,23 @@
 namespace ssd {
 namespace {
 
-constexpr int kTableChunk = 32;   // tokens per entry of the chunk table
+// The chunked kernels from this many tokens on: below it the token recurrence, one launch, is as
+// fast.
+constexpr int kChunkTokens = 24;
+
+bool chunked(const ssd_shape *s)
+{
+    return delta_chunk_supported(s->dtype == SSD_BF16, (int)s->headdim, (int)s->dstate) &&
+           s->seqlen >= kChunkTokens;
+}
+
+// Bytes of the chunks' items over all heads.
+size_t items_bytes(const ssd_shape *s, int64_t chunks, bool for_backward)
+{
+    return (size_t)(s->batch * chunks * s->nheads) * DeltaItem::bytes(for_backward);
+}
+
+int64_t chunks_of(const ssd_shape *s) { return (s->seqlen + kDeltaChunk - 1) / kDeltaChunk; }
 
 ssd_status check_delta(const ssd_shape *s, const ssd_delta_options *o, bool need_seq)
 {
@@ -17,8 +33,8 @@ ssd_status check_delta(const ssd_shape *s, const ssd_delta_options *o, bool need
                         "(got %lld)", (long long)s->dstate);
     if (o && o->qk_l2norm != 0 && o->qk_l2norm != 1)
         return api_fail(SSD_ERR_INVALID_ARG, "qk_l2norm must be 0 or 1");
-    const int64_t blocks = (s->headdim + 31) / 32;
-    if (s->batch * s->nheads * blocks > 0x7fffffffLL)
+    const int64_t blocks = (s->headdim + 15) / 16;   // of the launch grid, per batch row and head
+    if (s->batch * s->nheads * blocks > 0x7fffffffLL || s->seqlen > (int64_t)1 << 36)
         return api_fail(SSD_ERR_UNSUPPORTED, "problem too large for one launch grid");
     return SSD_OK;
 }
@@ -44,18 +60,19 @@ DeltaArgs delta_args(const ssd_shape *s, const ssd_delta_options *o, const void 
 }
 
 struct VarlenWs {
-    size_t status, tab, cstart, total;
+    size_t status, tab, cstart, items, total;
     int64_t slots;
 };
 
 VarlenWs varlen_ws(const ssd_shape *s, int nseq)
 {
     VarlenWs w;
-    w.slots = s->seqlen / kTableChunk + nseq;
+    w.slots = s->seqlen / kDeltaChunk + nseq;
     w.status = 0;
     w.tab = 256;
     w.cstart = w.tab + api_round256((size_t)w.slots * sizeof(int2));
-    w.total = w.cstart + api_round256((size_t)(nseq + 1) * sizeof(int32_t));
+    w.items = w.cstart + api_round256((size_t)(nseq + 1) * sizeof(int32_t));
+    w.total = w.items + (chunked(s) ? items_bytes(s, w.slots, false) : 0);
     return w;
 }
 
@@ -69,7 +86,7 @@ ssd_status check_delta_varlen(const ssd_shape *s, int nseq, const ssd_delta_opti
     if (nseq < 1) return api_fail(SSD_ERR_INVALID_ARG, "nseq must be >= 1 (got %d)", nseq);
     if (s->seqlen > 0x7fffffffLL - 256)
         return api_fail(SSD_ERR_UNSUPPORTED, "packed token count must fit int32 cu_seqlens");
-    if ((int64_t)nseq * s->nheads * 4 > 0x7fffffffLL)
+    if ((int64_t)nseq * s->nheads * 8 > 0x7fffffffLL)
         return api_fail(SSD_ERR_UNSUPPORTED, "problem too large for one launch grid");
     return SSD_OK;
 }
@@ -104,7 +121,7 @@ extern "C" {
 size_t ssd_delta_rule_workspace_size(const ssd_shape *shape)
 {
     if (check_delta(shape, nullptr, true) != SSD_OK) return 0;
-    return 256;
+    return 256 + (chunked(shape) ? items_bytes(shape, chunks_of(shape), false) : 0);
 }
 
 ssd_status ssd_delta_rule_fwd(const ssd_shape *shape, const void *q, const void *k,
@@ -137,7 +154,14 @@ ssd_status ssd_delta_rule_fwd(const ssd_shape *shape, const void *q, const void 
     if (workspace_bytes < need)
         return api_fail(SSD_ERR_INVALID_ARG, "workspace too small: need %zu bytes, got %zu", need,
                         workspace_bytes);
-    e = launch_delta_recurrent(a, s.dtype == SSD_BF16, nullptr, cst);
+    if (chunked(&s)) {
+        char *items = static_cast<char *>(workspace) + 256;
+        e = launch_delta_prep(a, items, false, chunks_of(&s), nullptr, cst);
+        if (e == cudaSuccess)
+            e = launch_delta_chain(a, items, chunks_of(&s), nullptr, nullptr, nullptr, cst);
+    } else {
+        e = launch_delta_recurrent(a, s.dtype == SSD_BF16, nullptr, cst);
+    }
     return e == cudaSuccess ? SSD_OK : api_cuda_fail(e, "delta rule launch");
 }
 
@@ -176,11 +200,17 @@ ssd_status ssd_delta_rule_varlen_fwd(const ssd_shape *shape, const void *q, cons
     cudaStream_t cst = static_cast<cudaStream_t>(stream);
     char *ws = static_cast<char *>(workspace);
     int *status = reinterpret_cast<int *>(ws + w.status);
-    cudaError_t e = launch_build_chunk_table(
-        cu_seqlens, nseq, a.L, kTableChunk, w.slots, reinterpret_cast<int2 *>(ws + w.tab),
-        reinterpret_cast<int32_t *>(ws + w.cstart), status, cst);
-    if (e == cudaSuccess)
+    int2 *tab = reinterpret_cast<int2 *>(ws + w.tab);
+    int32_t *cstart = reinterpret_cast<int32_t *>(ws + w.cstart);
+    cudaError_t e = launch_build_chunk_table(cu_seqlens, nseq, a.L, kDeltaChunk, w.slots, tab,
+                                             cstart, status, cst);
+    if (e == cudaSuccess && chunked(shape)) {
+        e = launch_delta_prep(a, ws + w.items, false, w.slots, tab, cst);
+        if (e == cudaSuccess)
+            e = launch_delta_chain(a, ws + w.items, w.slots, tab, cstart, status, cst);
+    } else if (e == cudaSuccess) {
         e = launch_delta_recurrent(a, shape->dtype == SSD_BF16, status, cst);
+    }
     return e == cudaSuccess ? SSD_OK : api_cuda_fail(e, "delta rule launch");
 }
 

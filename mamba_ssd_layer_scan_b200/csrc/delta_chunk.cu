@@ -1,0 +1,501 @@
+// The gated delta rule in chunks of 32 tokens (bf16 inputs).
+//
+// With cs the chunk's running sum of g, e_i = exp(cs_i), E = e_last, k and q as normalised where
+// that is asked for, and S the state that enters the chunk, the values that the tokens write are
+//
+//     W = Inv (V - e K S^T),   Inv = (I + A)^-1,   A_ij = exp(cs_i - cs_j) (k_i . k_j) beta_j, j < i
+//     O = scale e Q S^T + Att W,                   Att_ij = scale exp(cs_i - cs_j) (q_i . k_j) beta_j, j <= i
+//     S' = E S + sum_j (E / e_j) beta_j W_j k_j^T
+//
+// Two kernels.  delta_prep_kernel, parallel over chunks and heads, writes Inv - I, Att and the
+// factors of the rows (norms, decays, beta) -- everything that does not need the state.
+// delta_chain_kernel walks a sequence's chunks with the state in registers.  The rows p of a state
+// are independent of one another, and of U, O and the products with them too: a warp owns 16 rows
+// (the transposed products W^T = R^T Inv^T, S K^T, ... have p on the accumulators' rows), and the
+// layout in which one product leaves its accumulators is the A operand of the next, so the whole
+// chain of a chunk runs inside a warp with no exchange between warps at all.  They share the tiles
+// of K, Q, V and the triangles, which cp.async brings one chunk ahead.
+//
+// Accuracy: K, Q and V enter as they are; the state, the residual, W and Inv, which are float32,
+// enter as two bf16 parts each (2^-16), so that the state is carried to float32's usual accuracy:
+// 146 of the 184 matrix instructions per warp and chunk (P = 64, N = 128).  The output, rounded to
+// bf16 at once, takes the first parts only.
+//
+// Bound: the rate of the warp-level matrix instructions (one m16n8k16 in 8 cycles per SM quarter).
+#include "delta.cuh"
+#include "delta_mma.cuh"
+
+namespace ssd {
+namespace {
+
+using namespace sm100;
+
+constexpr int C = kDeltaChunk;
+constexpr int kPrepWarps = 4;
+constexpr int kPrepHeads = 16;     // heads of a group per CTA of the prep kernel
+constexpr float kMinDecay = -200.f;    // exp of it is 0 in float32
+constexpr float kMinBeta = 1e-20f;
+
+__device__ __forceinline__ float warp_sum4(float v)   // over 4 neighbouring lanes
+{
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+// a + b = s + err exactly
+__device__ __forceinline__ void two_sum(float a, float b, float &s, float &err)
+{
+    s = a + b;
+    const float bb = s - a;
+    err = (a - (s - bb)) + (b - bb);
+}
+
+// grid: (chunks, batch, G * head runs).  kBwd: also the second part of Att, and beta kept away
+// from 0, where the backward divides by it (a token of beta 1e-20 writes nothing either).
+template <int N, bool kBwd>
+__global__ void __launch_bounds__(kPrepWarps * 32)
+delta_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, const int2 *tab)
+{
+    constexpr int kPitch = N + 8;   // elements; 16 bytes more than a row: no bank conflicts
+    __shared__ __align__(16) bf16 ks[C * kPitch], qs[C * kPitch];
+    __shared__ float kk[C][C + 1], qk[C][C + 1];
+    __shared__ __align__(16) float As[kPrepWarps][C][C + 4];
+    __shared__ float rqs[C];
+
+    const int64_t c = blockIdx.x, b = blockIdx.y;
+    const int hpg = a.H / a.G, runs = (hpg + kPrepHeads - 1) / kPrepHeads;
+    const int g = blockIdx.z / runs, run = blockIdx.z % runs;
+    int64_t t0;
+    int len;
+    chunk_span(tab, c, C, a.L, t0, len);
+    if (len <= 0) return;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int64_t row0 = b * a.L + t0;
+
+    const bf16 *kg = static_cast<const bf16 *>(a.k) + (row0 * a.G + g) * N;
+    const bf16 *qg = static_cast<const bf16 *>(a.q) + (row0 * a.G + g) * N;
+    for (int i = tid; i < C * (N / 8); i += kPrepWarps * 32) {
+        const int r = i / (N / 8), col = i % (N / 8) * 8;
+        const int64_t off = r < len ? (int64_t)r * a.G * N + col : 0;
+        cp16(smem_u32(ks + r * kPitch + col), kg + off, r < len);
+        cp16(smem_u32(qs + r * kPitch + col), qg + off, r < len);
+    }
+    cp_commit();
+    cp_wait<0>();
+    __syncthreads();
+
+    {   // K K^T (warps 0, 1) and Q K^T (warps 2, 3), 16 rows each
+        const bf16 *rows = warp < 2 ? ks : qs;
+        const int m0 = (warp & 1) * 16;
+        float acc[4][4] = {};
+#pragma unroll
+        for (int s = 0; s < N / 16; ++s) {
+            uint32_t fa[4], fb[4];
+            ldsm4(fa, smem_u32(rows + (m0 + lane % 16) * kPitch + s * 16 + lane / 16 * 8));
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                ldsm4(fb, smem_u32(ks + (n * 16 + lane % 8 + lane / 16 * 8) * kPitch + s * 16 +
+                                   (lane / 8 & 1) * 8));
+                mma_16816(acc[2 * n], fa, fb[0], fb[1]);
+                mma_16816(acc[2 * n + 1], fa, fb[2], fb[3]);
+            }
+        }
+        float (*out)[C + 1] = warp < 2 ? kk : qk;
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                out[m0 + lane / 4 + r / 2 * 8][n * 8 + lane % 4 * 2 + r % 2] = acc[n][r];
+    }
+    if (a.l2norm) {   // |q|^2 of 8 tokens per warp, 4 lanes to a token (|k|^2: kk's diagonal)
+        const int r = warp * 8 + lane / 4;
+        float s = 0.f;
+        for (int i = lane % 4 * 2; i < N; i += 8) {
+            const uint32_t v = *reinterpret_cast<const uint32_t *>(qs + r * kPitch + i);
+            s = fmaf(bf16_lo(v), bf16_lo(v), s);
+            s = fmaf(bf16_hi(v), bf16_hi(v), s);
+        }
+        s = warp_sum4(s);
+        if (lane % 4 == 0) rqs[r] = rsqrtf(s + kL2Eps);
+    }
+    __syncthreads();
+
+    // a head per warp; lane j is token j: column j of the triangles
+    const bool on = lane < len;
+    const float rk = a.l2norm ? rsqrtf(kk[lane][lane] + kL2Eps) : 1.f;
+    const float rq = (a.l2norm ? rqs[lane] : 1.f) * a.scale;
+    float (*A)[C + 4] = As[warp];
+    const int h_end = min(hpg, (run + 1) * kPrepHeads);
+    for (int hl = run * kPrepHeads + warp; hl < h_end; hl += kPrepWarps) {
+        const int h = g * hpg + hl;
+        const int64_t at = (row0 + lane) * a.H + h;
+        float gt = on && a.g ? a.g[at] : 0.f;
+        float beta = on ? a.beta[at] : 0.f;
+        if (gt < kMinDecay) gt = kMinDecay;
+        if (kBwd && on && fabsf(beta) < kMinBeta) beta = kMinBeta;
+        // running sum of g in two floats: differences behind a token that wipes the state out
+        // (-200) stay accurate
+        float cs = gt, cl = 0.f;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float up = __shfl_up_sync(0xffffffffu, cs, o);
+            const float ul = __shfl_up_sync(0xffffffffu, cl, o);
+            if (lane >= o) {
+                float s, e;
+                two_sum(cs, up, s, e);
+                cs = s;
+                cl += ul + e;
+            }
+        }
+        const float cs_end = __shfl_sync(0xffffffffu, cs, 31);
+        const float cl_end = __shfl_sync(0xffffffffu, cl, 31);
+        const float e = __expf(cs + cl);
+        char *item = items + ((b * nchunks + c) * a.H + h) * DeltaItem::bytes(kBwd);
+        float *vec = reinterpret_cast<float *>(item + DeltaItem::kVec);
+        vec[lane] = on ? e * rk : 0.f;
+        vec[C + lane] = on ? __expf((cs_end - cs) + (cl_end - cl)) * rk * beta : 0.f;
+        vec[2 * C + lane] = on ? e * rq : 0.f;
+        if (lane == 31) vec[3 * C] = e;   // tokens past the end have g = 0
+
+        float x[C], att[C];
+        const float kb = rk * beta;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const float ci = __shfl_sync(0xffffffffu, cs, i), li = __shfl_sync(0xffffffffu, cl, i);
+            const float ri = __shfl_sync(0xffffffffu, rk, i), qi = __shfl_sync(0xffffffffu, rq, i);
+            const float d = lane <= i ? __expf((ci - cs) + (li - cl)) * kb : 0.f;
+            A[i][lane] = lane < i ? kk[i][lane] * ri * d : 0.f;
+            att[i] = lane <= i ? qk[i][lane] * qi * d : 0.f;
+            x[i] = 0.f;
+        }
+        __syncwarp();
+        // column `lane` of Inv by forward substitution: x_i = [i = lane] - sum_{k < i} A_ik x_k
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            float s0 = i == lane ? 1.f : 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+            for (int k = 0; k < i; k += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(&A[i][k]);
+                s0 = fmaf(-v.x, x[k], s0);
+                s1 = fmaf(-v.y, x[k + 1], s1);
+                s2 = fmaf(-v.z, x[k + 2], s2);
+                s3 = fmaf(-v.w, x[k + 3], s3);
+            }
+            x[i] = (s0 + s1) + (s2 + s3);
+        }
+        __syncwarp();
+        // rows i and i + 1, two columns to a lane: even lanes store row i, odd ones row i + 1
+#pragma unroll
+        for (int i = 0; i < C; i += 2) {
+            const float x0 = i == lane ? 0.f : x[i], x1 = i + 1 == lane ? 0.f : x[i + 1];
+            const bool odd = lane & 1;
+            const float xo = __shfl_xor_sync(0xffffffffu, odd ? x0 : x1, 1);
+            const float ao = __shfl_xor_sync(0xffffffffu, odd ? att[i] : att[i + 1], 1);
+            const int off = ((i + odd) * C + (lane & ~1)) * 2;
+            uint32_t hi, lo;
+            split2(odd ? xo : x0, odd ? x1 : xo, hi, lo);
+            *reinterpret_cast<uint32_t *>(item + DeltaItem::kInvHi + off) = hi;
+            *reinterpret_cast<uint32_t *>(item + DeltaItem::kInvLo + off) = lo;
+            split2(odd ? ao : att[i], odd ? att[i + 1] : ao, hi, lo);
+            *reinterpret_cast<uint32_t *>(item + DeltaItem::kAttHi + off) = hi;
+            if (kBwd) *reinterpret_cast<uint32_t *>(item + DeltaItem::kAttLo + off) = lo;
+        }
+    }
+}
+
+// Shared-memory stage of one chunk: K and Q of the group, then per head of the CTA its V, its
+// triangles and its factors.  Rows are 16 bytes longer than their data.
+struct ChainStage {
+    int kpitch, vpitch, head, total;   // bytes
+    static constexpr int kTriPitch = C * 2 + 16;
+    static constexpr int kTri = C * kTriPitch;
+    __host__ __device__ ChainStage(int rows, int N, int heads)
+        : kpitch(N * 2 + 16), vpitch(rows * 2 + 16), head(C * (rows * 2 + 16) + 3 * kTri + 512),
+          total(2 * C * (N * 2 + 16) + heads * head)
+    {
+    }
+};
+
+// A CTA has `heads` heads of one group and of each `rows` rows p: heads * rows / 16 warps.
+// grid: (sequences * H / heads * P / rows)
+template <int N>
+__global__ void __launch_bounds__(256)
+delta_chain_kernel(const DeltaArgs a, const char *items, int64_t nchunks, const int2 *tab,
+                   const int32_t *cstart, const int *status, int heads, int rows)
+{
+    extern __shared__ __align__(128) char smem[];
+    if (status && *status) return;
+    constexpr int NT = N / 8;
+    const int P = a.P;
+    const ChainStage lay(rows, N, heads);
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int splits = P / rows, blocks = a.H / heads * splits;
+    const int pb = (int)(blockIdx.x % splits) * rows;            // the CTA's first row
+    const int hl = warp / (rows / 16), pl = warp % (rows / 16) * 16;   // this warp's head, rows
+    const int p0 = pb + pl;
+    const int h0 = (int)(blockIdx.x % blocks) / splits * heads;
+    const int64_t seq = blockIdx.x / blocks;
+    const int h = h0 + hl, g = h0 / (a.H / a.G);
+    const int64_t b = cstart ? 0 : seq;
+    const int64_t c_begin = cstart ? cstart[seq] : 0, c_end = cstart ? cstart[seq + 1] : nchunks;
+
+    float S[NT][4];
+    const int64_t srow = ((seq * a.H + h) * P + p0 + lane / 4) * N + lane % 4 * 2;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        float2 u = make_float2(0.f, 0.f), v = u;
+        if (a.init) {
+            u = *reinterpret_cast<const float2 *>(a.init + srow + n * 8);
+            v = *reinterpret_cast<const float2 *>(a.init + srow + 8 * N + n * 8);
+        }
+        S[n][0] = u.x; S[n][1] = u.y; S[n][2] = v.x; S[n][3] = v.y;
+    }
+
+    const uint32_t base = smem_u32(smem);
+    auto load = [&](int64_t c, int stage) {
+        int64_t t0;
+        int len;
+        chunk_span(tab, c, C, a.L, t0, len);
+        const int64_t row0 = b * a.L + t0;
+        const uint32_t s = base + stage * lay.total;
+        const int nthr = blockDim.x;
+        const bf16 *kg = static_cast<const bf16 *>(a.k) + (row0 * a.G + g) * N;
+        const bf16 *qg = static_cast<const bf16 *>(a.q) + (row0 * a.G + g) * N;
+        for (int i = tid; i < C * (N / 8); i += nthr) {
+            const int r = i / (N / 8), col = i % (N / 8);
+            const bool on = r < len;
+            const int64_t off = on ? (int64_t)r * a.G * N + col * 8 : 0;
+            cp16(s + r * lay.kpitch + col * 16, kg + off, on);
+            cp16(s + (C + r) * lay.kpitch + col * 16, qg + off, on);
+        }
+        for (int x = 0; x < heads; ++x) {
+            const uint32_t sh = s + 2 * C * lay.kpitch + x * lay.head;
+            const bf16 *vg = static_cast<const bf16 *>(a.v) + (row0 * a.H + h0 + x) * P + pb;
+            const int pieces = rows / 8;
+            for (int i = tid; i < C * pieces; i += nthr) {
+                const int r = i / pieces, col = i % pieces;
+                const bool on = r < len;
+                cp16(sh + r * lay.vpitch + col * 16,
+                     vg + (on ? (int64_t)r * a.H * P + col * 8 : 0), on);
+            }
+            const char *item =
+                items + ((b * nchunks + c) * a.H + h0 + x) * DeltaItem::bytes(false);
+            const uint32_t tri = sh + C * lay.vpitch;
+            for (int i = tid; i < 3 * C * 4 + 32; i += nthr) {
+                if (i < 3 * C * 4) {   // Inv's two parts, Att: rows of four 16-byte pieces
+                    const int m = i / (C * 4), r = i / 4 % C, col = i % 4;
+                    const int src = (m == 2 ? DeltaItem::kAttHi : m * DeltaItem::kTri);
+                    cp16(tri + m * ChainStage::kTri + r * ChainStage::kTriPitch + col * 16,
+                         item + src + r * C * 2 + col * 16, true);
+                } else {
+                    const int j = i - 3 * C * 4;
+                    cp16(tri + 3 * ChainStage::kTri + j * 16, item + DeltaItem::kVec + j * 16,
+                         true);
+                }
+            }
+        }
+    };
+
+    if (c_begin < c_end) load(c_begin, 0);
+    cp_commit();
+    // fragment addresses inside a stage
+    const int row_nn = lane % 8 + lane / 16 * 8, col_nn = (lane / 8 & 1) * 16;   // rows on n
+    const int row_kk = lane % 8 + (lane / 8 & 1) * 8, col_kk = lane / 16 * 16;   // rows on k
+    for (int64_t c = c_begin; c < c_end; ++c) {
+        const int stage = (int)(c - c_begin) & 1;
+        cp_wait<0>();
+        __syncthreads();   // this chunk has arrived; everyone is done with the other stage
+        if (c + 1 < c_end) load(c + 1, stage ^ 1);
+        cp_commit();
+
+        const uint32_t ks = base + stage * lay.total, qs = ks + C * lay.kpitch;
+        const uint32_t vs = qs + C * lay.kpitch + hl * lay.head;
+        const uint32_t inv = vs + C * lay.vpitch, att = inv + 2 * ChainStage::kTri;
+        const float *vec = reinterpret_cast<const float *>(
+            smem + stage * lay.total + 2 * C * lay.kpitch + hl * lay.head + C * lay.vpitch +
+            3 * ChainStage::kTri);
+
+        // S K^T and S Q^T (columns: tokens)
+        float X[4][4] = {}, O[4][4] = {};
+#pragma unroll
+        for (int s = 0; s < N / 16; ++s) {
+            uint32_t hi[4], lo[4], fb[4];
+            split_a(S[2 * s], S[2 * s + 1], hi, lo);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                ldsm4(fb, ks + (n * 16 + row_nn) * lay.kpitch + s * 32 + col_nn);
+                mma_16816(X[2 * n], hi, fb[0], fb[1]);
+                mma_16816(X[2 * n + 1], hi, fb[2], fb[3]);
+                mma_16816(X[2 * n], lo, fb[0], fb[1]);
+                mma_16816(X[2 * n + 1], lo, fb[2], fb[3]);
+                ldsm4(fb, qs + (n * 16 + row_nn) * lay.kpitch + s * 32 + col_nn);
+                mma_16816(O[2 * n], hi, fb[0], fb[1]);
+                mma_16816(O[2 * n + 1], hi, fb[2], fb[3]);
+            }
+        }
+        // R = V - e K S^T, in place of S K^T; the output's part from the state takes its factor
+        const uint32_t vaddr = vs + pl * 2 + row_nn * lay.vpitch + col_nn;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            uint32_t fv[4];
+            ldsm4_trans(fv, vaddr + n * 16 * lay.vpitch);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const int t = 2 * n + m;
+                const float2 ek = *reinterpret_cast<const float2 *>(vec + t * 8 + lane % 4 * 2);
+                const float2 eq =
+                    *reinterpret_cast<const float2 *>(vec + 2 * C + t * 8 + lane % 4 * 2);
+                X[t][0] = fmaf(-ek.x, X[t][0], bf16_lo(fv[2 * m]));
+                X[t][1] = fmaf(-ek.y, X[t][1], bf16_hi(fv[2 * m]));
+                X[t][2] = fmaf(-ek.x, X[t][2], bf16_lo(fv[2 * m + 1]));
+                X[t][3] = fmaf(-ek.y, X[t][3], bf16_hi(fv[2 * m + 1]));
+                O[t][0] *= eq.x; O[t][1] *= eq.y; O[t][2] *= eq.x; O[t][3] *= eq.y;
+            }
+        }
+        // W = R + (Inv - I) R: blocks of 16 tokens on and below the diagonal
+        float W[4][4];
+        {
+            uint32_t hi[2][4], lo[2][4];
+            split_a(X[0], X[1], hi[0], lo[0]);
+            split_a(X[2], X[3], hi[1], lo[1]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) W[t][r] = X[t][r];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int s = 0; s <= n; ++s) {
+                    uint32_t fh[4], fl[4];
+                    const uint32_t at =
+                        inv + (n * 16 + row_nn) * ChainStage::kTriPitch + s * 32 + col_nn;
+                    ldsm4(fh, at);
+                    ldsm4(fl, at + ChainStage::kTri);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        mma_16816(W[2 * n + m], hi[s], fh[2 * m], fh[2 * m + 1]);
+                        mma_16816(W[2 * n + m], lo[s], fh[2 * m], fh[2 * m + 1]);
+                        mma_16816(W[2 * n + m], hi[s], fl[2 * m], fl[2 * m + 1]);
+                    }
+                }
+        }
+        // O += Att W
+        {
+            uint32_t hi[2][4];
+            round_a(W[0], W[1], hi[0]);
+            round_a(W[2], W[3], hi[1]);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int s = 0; s <= n; ++s) {
+                    uint32_t fb[4];
+                    ldsm4(fb, att + (n * 16 + row_nn) * ChainStage::kTriPitch + s * 32 + col_nn);
+                    mma_16816(O[2 * n], hi[s], fb[0], fb[1]);
+                    mma_16816(O[2 * n + 1], hi[s], fb[2], fb[3]);
+                }
+        }
+        // S = E S + (E / e beta W)^T K
+        const float E = vec[3 * C];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[n][r] *= E;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const float2 sw = *reinterpret_cast<const float2 *>(vec + C + t * 8 + lane % 4 * 2);
+            W[t][0] *= sw.x; W[t][1] *= sw.y; W[t][2] *= sw.x; W[t][3] *= sw.y;
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            uint32_t hi[4], lo[4];
+            split_a(W[2 * s], W[2 * s + 1], hi, lo);
+#pragma unroll
+            for (int n = 0; n < NT / 2; ++n) {
+                uint32_t fb[4];
+                ldsm4_trans(fb, ks + (s * 16 + row_kk) * lay.kpitch + n * 32 + col_kk);
+                mma_16816(S[2 * n], hi, fb[0], fb[1]);
+                mma_16816(S[2 * n + 1], hi, fb[2], fb[3]);
+                mma_16816(S[2 * n], lo, fb[0], fb[1]);
+                mma_16816(S[2 * n + 1], lo, fb[2], fb[3]);
+            }
+        }
+        // the output through this warp's columns of the V tile, which nobody reads any more
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            uint32_t fo[4];
+            round_a(O[2 * n], O[2 * n + 1], fo);
+            stsm4_trans(vaddr + n * 16 * lay.vpitch, fo);
+        }
+        __syncwarp();
+        int64_t t0;
+        int len;
+        chunk_span(tab, c, C, a.L, t0, len);
+        bf16 *og = static_cast<bf16 *>(a.o) + ((b * a.L + t0) * a.H + h) * P + p0;
+#pragma unroll
+        for (int i = lane; i < C * 2; i += 32) {   // 32 bytes of a row: two lanes
+            const int r = i / 2, half = i % 2;
+            if (r < len) {
+                uint4 v;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                             : "r"(vs + pl * 2 + r * lay.vpitch + half * 16) : "memory");
+                *reinterpret_cast<uint4 *>(og + (int64_t)r * a.H * P + half * 8) = v;
+            }
+        }
+    }
+    cp_wait<0>();
+    if (a.final_state) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            *reinterpret_cast<float2 *>(a.final_state + srow + n * 8) =
+                make_float2(S[n][0], S[n][1]);
+            *reinterpret_cast<float2 *>(a.final_state + srow + 8 * N + n * 8) =
+                make_float2(S[n][2], S[n][3]);
+        }
+    }
+}
+
+}  // namespace
+
+bool delta_chunk_supported(bool is_bf16, int P, int N)
+{
+    return is_bf16 && (N == 64 || N == 128) && P % 16 == 0 && P <= 128;
+}
+
+cudaError_t launch_delta_prep(const DeltaArgs &a, char *items, bool for_backward, int64_t nchunks,
+                              const int2 *tab, cudaStream_t st)
+{
+    const int runs = (a.H / a.G + kPrepHeads - 1) / kPrepHeads;
+    const dim3 grid((unsigned)nchunks, (unsigned)(tab ? 1 : a.batch), (unsigned)(a.G * runs));
+    const dim3 block(kPrepWarps * 32);
+    if (a.N == 128) {
+        if (for_backward) delta_prep_kernel<128, true><<<grid, block, 0, st>>>(a, items, nchunks, tab);
+        else delta_prep_kernel<128, false><<<grid, block, 0, st>>>(a, items, nchunks, tab);
+    } else {
+        if (for_backward) delta_prep_kernel<64, true><<<grid, block, 0, st>>>(a, items, nchunks, tab);
+        else delta_prep_kernel<64, false><<<grid, block, 0, st>>>(a, items, nchunks, tab);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_delta_chain(const DeltaArgs &a, const char *items, int64_t nchunks,
+                               const int2 *tab, const int32_t *cstart, const int *status,
+                               cudaStream_t st)
+{
+    const int64_t nseq = cstart ? a.nseq : a.batch;
+    int heads = 1, rows = a.P;
+    while (nseq * a.H * (a.P / rows) < 148 && rows % 32 == 0) rows /= 2;
+    const unsigned grid = (unsigned)(nseq * (a.H / heads) * (a.P / rows));
+    const unsigned threads = (unsigned)(heads * rows / 16 * 32);
+    const int smem = 2 * ChainStage(rows, a.N, heads).total;
+    auto go = [&](auto kern) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        kern<<<grid, threads, smem, st>>>(a, items, nchunks, tab, cstart, status, heads,
+                                           rows);
+        return cudaGetLastError();
+    };
+    return a.N == 128 ? go(delta_chain_kernel<128>) : go(delta_chain_kernel<64>);
+}
+
+}  // namespace ssd

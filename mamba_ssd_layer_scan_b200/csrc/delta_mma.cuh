@@ -1,0 +1,78 @@
+// Warp-level bf16 matrix products of the gated delta rule's chunked kernels: fragments, the split
+// of a float32 into two bf16 parts, shared-memory tiles.
+#pragma once
+
+#include "sm100.cuh"
+
+namespace ssd {
+
+// D (16 x 8, float32) += A (16 x 16, bf16) B (16 x 8, bf16).  Lane l holds of D rows l/4 and
+// l/4 + 8, columns 2 (l % 4) + {0, 1}; of A the same rows, columns 2 (l % 4) + {0, 1, 8, 9}; of B
+// rows (k) 2 (l % 4) + {0, 1, 8, 9}, column l/4.  Two neighbouring D tiles are thus an A operand.
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+                 "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void stsm4_trans(uint32_t addr, const uint32_t (&r)[4])
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%4], {%0, %1, %2, %3};"
+                 ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// x and y as bf16 pairs: hi the roundings, lo the roundings of what they leave.  hi + lo is x to
+// 2^-16 of it: products with an exact bf16 operand then keep float32's usual accuracy.
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo)
+{
+    hi = sm100::pack_bf16x2(x, y);
+    lo = sm100::pack_bf16x2(x - bf16_lo(hi), y - bf16_hi(hi));
+}
+
+// The A operand made of two neighbouring D tiles.
+__device__ __forceinline__ void split_a(const float (&t0)[4], const float (&t1)[4],
+                                        uint32_t (&hi)[4], uint32_t (&lo)[4])
+{
+    split2(t0[0], t0[1], hi[0], lo[0]);
+    split2(t0[2], t0[3], hi[1], lo[1]);
+    split2(t1[0], t1[1], hi[2], lo[2]);
+    split2(t1[2], t1[3], hi[3], lo[3]);
+}
+__device__ __forceinline__ void round_a(const float (&t0)[4], const float (&t1)[4],
+                                        uint32_t (&hi)[4])
+{
+    hi[0] = sm100::pack_bf16x2(t0[0], t0[1]);
+    hi[1] = sm100::pack_bf16x2(t0[2], t0[3]);
+    hi[2] = sm100::pack_bf16x2(t1[0], t1[1]);
+    hi[3] = sm100::pack_bf16x2(t1[2], t1[3]);
+}
+
+// 16 bytes from global to shared memory; zeros where `on` is false (nothing is read then).
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool on)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft> __device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+}  // namespace ssd
