@@ -387,6 +387,35 @@ ssd_status ssd_delta_rule_varlen_fwd(const ssd_shape *shape, const void *q, cons
                                      size_t workspace_bytes, void *stream);
 
 /*
+ * Gradients of ssd_delta_rule_fwd with respect to every input, given dout (of o) and dfinal (of the
+ * final state, nullable: zero).  Nothing needs to be kept from the forward call: it is run again,
+ * with the state kept every 64 tokens.  With W_t = v_t - exp(g_t) S_{t-1} k_t, what the decayed
+ * state lacks of v_t, and G_t the gradient of S_t (its later uses and o_t):
+ *
+ *     dq_t = scale S_t^T dout_t              dv_t = beta_t G_t k_t        dbeta_t = W_t . G_t k_t
+ *     dk_t = beta_t G_t^T W_t - exp(g_t) S_{t-1}^T dv_t
+ *     dg_t = <G_t - dv_t k_t^T, exp(g_t) S_{t-1}>
+ *     G_{t-1} = exp(g_t) (G_t - dv_t k_t^T) + scale dout_{t-1} q_{t-1}^T
+ *
+ * (dq and dk summed over the heads of a group, and through the norm where qk_l2norm is set.)
+ *
+ *   dq, dk, dv   like q, k and v, in their type;  dg, dbeta (batch, seqlen, nheads) float32, dg
+ *                with g (NULL where g is);  dinit (batch, nheads, headdim, dstate) float32,
+ *                nullable.  No output may alias an input.  A beta nearer to 0 than 1e-20 is taken
+ *                as 1e-20.  Repeated calls give the same bits.
+ *   workspace    ssd_delta_rule_bwd_workspace_size bytes (0: invalid or unsupported), 256-byte
+ *                aligned.
+ * bf16, headdim a multiple of 16 and dstate 64 or 128; other shapes return SSD_ERR_UNSUPPORTED.
+ */
+size_t ssd_delta_rule_bwd_workspace_size(const ssd_shape *shape);
+ssd_status ssd_delta_rule_bwd(const ssd_shape *shape, const void *q, const void *k, const void *v,
+                              const float *g, const float *beta,
+                              const ssd_delta_options *options, const float *init_state,
+                              const void *dout, const float *dfinal, void *dq, void *dk, void *dv,
+                              float *dg, float *dbeta, float *dinit, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
  * One token per sequence (decode): state (batch, nheads, headdim, dstate) float32 is updated in
  * place; q, k (batch, ngroups, dstate), v, o (batch, nheads, headdim), g (nullable) and beta
  * (batch, nheads).  shape->seqlen is ignored.  state, q and k must be 16-byte aligned.

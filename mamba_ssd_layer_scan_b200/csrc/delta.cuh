@@ -47,8 +47,33 @@ struct DeltaItem {
 
 cudaError_t launch_delta_prep(const DeltaArgs &a, char *items, bool for_backward, int64_t nchunks,
                               const int2 *tab, cudaStream_t st);
-cudaError_t launch_delta_chain(const DeltaArgs &a, const char *items, int64_t nchunks,
-                               const int2 *tab, const int32_t *cstart, const int *status,
+// What the backward's kernels hand on through the workspace, and its outputs.  Spans are of 64
+// tokens (n64 per batch row), tiles the P / 16 runs of 16 rows of a head, chunks of 32 tokens.
+struct DeltaBwd {
+    const bf16 *dout;      // (batch, L, H, P)
+    const float *dfinal;   // (batch, H, P, N), nullable
+    int64_t n64;
+    float *states;         // (batch, n64 + 1, H, P, N): entering each span; last: the final state
+    bf16 *dstates;         // (batch, n64, H, P, N): the gradient of the state leaving each span
+    float *wfrag;          // W in accumulator layout, per (batch, chunk, H, tile): 16 x 32
+    bf16 *w;               // (batch, L, H, P): W
+    float *dot_oo, *dot_vv, *dot_vw;   // (batch, chunk, H, tile, 32): <dO, O>, <dV, V>, <dV, W>
+    float *dot_ss;         // (batch, n64, H, tile): <dS', S'>
+    float *dq_part, *dk_part;          // (batch, L, G * runs, N)
+    int runs;              // runs of heads per group, `run_heads` each (the last may be shorter)
+    int run_heads;
+    bf16 *dq, *dk, *dv;    // outputs
+    float *dg, *dbeta, *dinit;         // dg, dinit nullable
+};
+
+// bwd: nullable; with it the forward is run for the backward (see delta_chunk.cu).
+cudaError_t launch_delta_chain(const DeltaArgs &a, const DeltaBwd *bwd, const char *items,
+                               int64_t nchunks, const int2 *tab, const int32_t *cstart,
+                               const int *status, cudaStream_t st);
+cudaError_t launch_delta_adjoint(const DeltaArgs &a, const DeltaBwd &w, const char *items,
+                                 int64_t nchunks, cudaStream_t st);
+// dq and dk of each span and run of heads, then their sums over the runs; dg and dbeta.
+cudaError_t launch_delta_grads(const DeltaArgs &a, const DeltaBwd &w, int64_t nchunks,
                                cudaStream_t st);
 
 }  // namespace ssd

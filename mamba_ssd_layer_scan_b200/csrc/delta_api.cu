@@ -34,7 +34,8 @@ ssd_status check_delta(const ssd_shape *s, const ssd_delta_options *o, bool need
     if (o && o->qk_l2norm != 0 && o->qk_l2norm != 1)
         return api_fail(SSD_ERR_INVALID_ARG, "qk_l2norm must be 0 or 1");
     const int64_t blocks = (s->headdim + 15) / 16;   // of the launch grid, per batch row and head
-    if (s->batch * s->nheads * blocks > 0x7fffffffLL || s->seqlen > (int64_t)1 << 36)
+    if (s->batch * s->nheads * blocks > 0x7fffffffLL || s->seqlen > (int64_t)1 << 34 ||
+        s->batch * s->nheads * (s->seqlen / 32 + 1) > (int64_t)1 << 36)
         return api_fail(SSD_ERR_UNSUPPORTED, "problem too large for one launch grid");
     return SSD_OK;
 }
@@ -88,6 +89,60 @@ ssd_status check_delta_varlen(const ssd_shape *s, int nseq, const ssd_delta_opti
         return api_fail(SSD_ERR_UNSUPPORTED, "packed token count must fit int32 cu_seqlens");
     if ((int64_t)nseq * s->nheads * 8 > 0x7fffffffLL)
         return api_fail(SSD_ERR_UNSUPPORTED, "problem too large for one launch grid");
+    return SSD_OK;
+}
+
+// The backward's workspace: the items, then what the chains hand to the gradients' kernels.
+struct BwdWs {
+    size_t items, states, dstates, wfrag, w, dot_oo, dot_vv, dot_vw, dot_ss, dq, dk, total;
+    int64_t chunks, spans;
+    int runs, run_heads;
+};
+
+BwdWs bwd_ws(const ssd_shape *s)
+{
+    BwdWs w;
+    w.chunks = chunks_of(s);
+    w.spans = (s->seqlen + 63) / 64;
+    const size_t H = (size_t)s->nheads, PN = (size_t)(s->headdim * s->dstate);
+    const size_t items = (size_t)(s->batch * w.chunks) * H, spans = (size_t)(s->batch * w.spans) * H;
+    const size_t tiles = (size_t)s->headdim / 16, tokens = (size_t)(s->batch * s->seqlen);
+    // up to eight heads of a group per CTA of the gradients' kernel, whose sums stay in
+    // registers; fewer where the launch would leave SMs empty
+    const int hpg = (int)(s->nheads / s->ngroups);
+    w.run_heads = hpg < 8 ? hpg : 8;
+    auto runs = [&] { return (hpg + w.run_heads - 1) / w.run_heads; };
+    while (w.run_heads > 1 && s->batch * w.spans * s->ngroups * runs() < 296)
+        w.run_heads = (w.run_heads + 1) / 2;
+    w.runs = runs();
+    size_t at = 256;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += api_round256(bytes);
+        return here;
+    };
+    w.items = take(items * DeltaItem::bytes(true));
+    w.states = take((spans + (size_t)s->batch * H) * PN * 4);
+    w.dstates = take(spans * PN * 2);
+    w.wfrag = take(items * (size_t)s->headdim * kDeltaChunk * 4);
+    w.w = take(tokens * H * (size_t)s->headdim * 2);
+    w.dot_oo = take(items * tiles * kDeltaChunk * 4);
+    w.dot_vv = take(items * tiles * kDeltaChunk * 4);
+    w.dot_vw = take(items * tiles * kDeltaChunk * 4);
+    w.dot_ss = take(spans * tiles * 4);
+    w.dq = take(tokens * (size_t)(s->ngroups * w.runs) * (size_t)s->dstate * 4);
+    w.dk = take(tokens * (size_t)(s->ngroups * w.runs) * (size_t)s->dstate * 4);
+    w.total = at;
+    return w;
+}
+
+ssd_status check_delta_bwd(const ssd_shape *s, const ssd_delta_options *o)
+{
+    ssd_status st = check_delta(s, o, true);
+    if (st != SSD_OK) return st;
+    if (!delta_chunk_supported(s->dtype == SSD_BF16, (int)s->headdim, (int)s->dstate))
+        return api_fail(SSD_ERR_UNSUPPORTED, "the delta rule's backward needs bf16, headdim a "
+                        "multiple of 16 and dstate 64 or 128");
     return SSD_OK;
 }
 
@@ -158,7 +213,7 @@ ssd_status ssd_delta_rule_fwd(const ssd_shape *shape, const void *q, const void 
         char *items = static_cast<char *>(workspace) + 256;
         e = launch_delta_prep(a, items, false, chunks_of(&s), nullptr, cst);
         if (e == cudaSuccess)
-            e = launch_delta_chain(a, items, chunks_of(&s), nullptr, nullptr, nullptr, cst);
+            e = launch_delta_chain(a, nullptr, items, chunks_of(&s), nullptr, nullptr, nullptr, cst);
     } else {
         e = launch_delta_recurrent(a, s.dtype == SSD_BF16, nullptr, cst);
     }
@@ -207,11 +262,86 @@ ssd_status ssd_delta_rule_varlen_fwd(const ssd_shape *shape, const void *q, cons
     if (e == cudaSuccess && chunked(shape)) {
         e = launch_delta_prep(a, ws + w.items, false, w.slots, tab, cst);
         if (e == cudaSuccess)
-            e = launch_delta_chain(a, ws + w.items, w.slots, tab, cstart, status, cst);
+            e = launch_delta_chain(a, nullptr, ws + w.items, w.slots, tab, cstart, status, cst);
     } else if (e == cudaSuccess) {
         e = launch_delta_recurrent(a, shape->dtype == SSD_BF16, status, cst);
     }
     return e == cudaSuccess ? SSD_OK : api_cuda_fail(e, "delta rule launch");
+}
+
+size_t ssd_delta_rule_bwd_workspace_size(const ssd_shape *shape)
+{
+    if (check_delta_bwd(shape, nullptr) != SSD_OK) return 0;
+    return bwd_ws(shape).total;
+}
+
+ssd_status ssd_delta_rule_bwd(const ssd_shape *shape, const void *q, const void *k, const void *v,
+                              const float *g, const float *beta,
+                              const ssd_delta_options *options, const float *init_state,
+                              const void *dout, const float *dfinal, void *dq, void *dk, void *dv,
+                              float *dg, float *dbeta, float *dinit, void *workspace,
+                              size_t workspace_bytes, void *stream)
+{
+    if (!options) return api_fail(SSD_ERR_INVALID_ARG, "options is NULL");
+    ssd_status st = check_delta_bwd(shape, options);
+    if (st == SSD_OK) st = check_states(init_state, nullptr);
+    if (st == SSD_OK) st = check_states(dfinal, dinit);
+    if (st != SSD_OK) return st;
+    const ssd_shape s = *shape;
+    cudaStream_t cst = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (s.batch == 0) return SSD_OK;
+    if (s.seqlen == 0) {   // the final state is the initial one
+        if (!dinit) return SSD_OK;
+        e = launch_fill_final(dfinal, dinit, s.batch * s.nheads * s.headdim * s.dstate, cst);
+        return e == cudaSuccess ? SSD_OK : api_cuda_fail(e, "fill dinit");
+    }
+    DeltaArgs a = delta_args(&s, options, q, k, v, g, beta);
+    a.init = init_state;
+    a.o = dv;   // checked like the forward's output
+    st = check_pointers(a, workspace);
+    if (st != SSD_OK) return st;
+    a.o = nullptr;
+    if (!dout || !dq || !dk || !dbeta || (g != nullptr) != (dg != nullptr))
+        return api_fail(SSD_ERR_INVALID_ARG,
+                        "dout, dq, dk and dbeta must be non-NULL, and dg go with g");
+    if (!api_aligned(dout, 16) || !api_aligned(dq, 16) || !api_aligned(dk, 16))
+        return api_fail(SSD_ERR_INVALID_ARG, "dout, dq and dk must be 16-byte aligned");
+    const BwdWs l = bwd_ws(&s);
+    if (workspace_bytes < l.total)
+        return api_fail(SSD_ERR_INVALID_ARG, "workspace too small: need %zu bytes, got %zu",
+                        l.total, workspace_bytes);
+    char *ws = static_cast<char *>(workspace);
+    auto f32 = [&](size_t at) { return reinterpret_cast<float *>(ws + at); };
+    DeltaBwd w = {};
+    w.dout = static_cast<const bf16 *>(dout);
+    w.dfinal = dfinal;
+    w.n64 = l.spans;
+    w.states = f32(l.states);
+    w.dstates = reinterpret_cast<bf16 *>(ws + l.dstates);
+    w.wfrag = f32(l.wfrag);
+    w.w = reinterpret_cast<bf16 *>(ws + l.w);
+    w.dot_oo = f32(l.dot_oo);
+    w.dot_vv = f32(l.dot_vv);
+    w.dot_vw = f32(l.dot_vw);
+    w.dot_ss = f32(l.dot_ss);
+    w.dq_part = f32(l.dq);
+    w.dk_part = f32(l.dk);
+    w.runs = l.runs;
+    w.run_heads = l.run_heads;
+    w.dq = static_cast<bf16 *>(dq);
+    w.dk = static_cast<bf16 *>(dk);
+    w.dv = static_cast<bf16 *>(dv);
+    w.dg = dg;
+    w.dbeta = dbeta;
+    w.dinit = dinit;
+    char *items = ws + l.items;
+    e = launch_delta_prep(a, items, true, l.chunks, nullptr, cst);
+    if (e == cudaSuccess)
+        e = launch_delta_chain(a, &w, items, l.chunks, nullptr, nullptr, nullptr, cst);
+    if (e == cudaSuccess) e = launch_delta_adjoint(a, w, items, l.chunks, cst);
+    if (e == cudaSuccess) e = launch_delta_grads(a, w, l.chunks, cst);
+    return e == cudaSuccess ? SSD_OK : api_cuda_fail(e, "delta rule backward launch");
 }
 
 ssd_status ssd_delta_rule_update(const ssd_shape *shape, float *state, const void *q,

@@ -203,97 +203,190 @@ delta_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, const int2 *t
     }
 }
 
-// Shared-memory stage of one chunk: K and Q of the group, then per head of the CTA its V, its
-// triangles and its factors.  Rows are 16 bytes longer than their data.
+// Shared-memory stage of one chunk: K and Q of the group, then per head of the CTA its V (and dO,
+// for the backward), its triangles and its factors.  Rows are 16 bytes longer than their data.
 struct ChainStage {
-    int kpitch, vpitch, head, total;   // bytes
+    int kpitch, vpitch, tri, vec, head, total;   // bytes; tri, vec: offsets in a head's part
     static constexpr int kTriPitch = C * 2 + 16;
     static constexpr int kTri = C * kTriPitch;
-    __host__ __device__ ChainStage(int rows, int N, int heads)
-        : kpitch(N * 2 + 16), vpitch(rows * 2 + 16), head(C * (rows * 2 + 16) + 3 * kTri + 512),
-          total(2 * C * (N * 2 + 16) + heads * head)
+    __host__ __device__ ChainStage(int rows, int N, int heads, bool bwd)
+        : kpitch(N * 2 + 16), vpitch(rows * 2 + 16), tri((bwd ? 2 : 1) * C * (rows * 2 + 16)),
+          vec(tri + (bwd ? 4 : 3) * kTri), head(vec + 512), total(2 * C * kpitch + heads * head)
     {
     }
 };
 
+// The CTA's share of a launch: see delta_chain_kernel.
+struct ChainSlice {
+    int64_t b, seq;
+    int h0, g, pb, heads, rows;
+    __device__ ChainSlice(const DeltaArgs &a, int heads_, int rows_, bool packed)
+        : heads(heads_), rows(rows_)
+    {
+        const int splits = a.P / rows, blocks = a.H / heads * splits;
+        pb = (int)(blockIdx.x % splits) * rows;
+        h0 = (int)(blockIdx.x % blocks) / splits * heads;
+        seq = blockIdx.x / blocks;
+        g = h0 / (a.H / a.G);
+        b = packed ? 0 : seq;
+    }
+};
+
+// Issues the copies of chunk c into the stage at shared address s.
+template <int N, bool kBwd>
+__device__ __forceinline__ void load_stage(const DeltaArgs &a, const ChainStage &lay,
+                                           const ChainSlice &w, const char *items,
+                                           const bf16 *dout, int64_t nchunks, const int2 *tab,
+                                           int64_t c, uint32_t s)
+{
+    int64_t t0;
+    int len;
+    chunk_span(tab, c, C, a.L, t0, len);
+    const int64_t row0 = w.b * a.L + t0;
+    const int tid = threadIdx.x, nthr = blockDim.x;
+    const bf16 *kg = static_cast<const bf16 *>(a.k) + (row0 * a.G + w.g) * N;
+    const bf16 *qg = static_cast<const bf16 *>(a.q) + (row0 * a.G + w.g) * N;
+    for (int i = tid; i < C * (N / 8); i += nthr) {
+        const int r = i / (N / 8), col = i % (N / 8);
+        const bool on = r < len;
+        const int64_t off = on ? (int64_t)r * a.G * N + col * 8 : 0;
+        cp16(s + r * lay.kpitch + col * 16, kg + off, on);
+        cp16(s + (C + r) * lay.kpitch + col * 16, qg + off, on);
+    }
+    for (int x = 0; x < w.heads; ++x) {
+        const uint32_t sh = s + 2 * C * lay.kpitch + x * lay.head;
+        const int64_t vat = (row0 * a.H + w.h0 + x) * a.P + w.pb;
+        const bf16 *vg = static_cast<const bf16 *>(a.v) + vat;
+        const int pieces = w.rows / 8;
+        for (int i = tid; i < C * pieces; i += nthr) {
+            const int r = i / pieces, col = i % pieces;
+            const bool on = r < len;
+            const int64_t off = on ? (int64_t)r * a.H * a.P + col * 8 : 0;
+            cp16(sh + r * lay.vpitch + col * 16, vg + off, on);
+            if (kBwd) cp16(sh + (C + r) * lay.vpitch + col * 16, dout + vat + off, on);
+        }
+        const char *item = items + ((w.b * nchunks + c) * a.H + w.h0 + x) * DeltaItem::bytes(kBwd);
+        constexpr int kTris = kBwd ? 4 : 3;
+        for (int i = tid; i < kTris * C * 4 + 32; i += nthr) {
+            if (i < kTris * C * 4) {   // Inv's two parts, Att's: rows of four 16-byte pieces
+                const int m = i / (C * 4), r = i / 4 % C, col = i % 4;
+                const int src = m < 2 ? m * DeltaItem::kTri
+                                      : DeltaItem::kAttHi + (m - 2) * DeltaItem::kTri;
+                cp16(sh + lay.tri + m * ChainStage::kTri + r * ChainStage::kTriPitch + col * 16,
+                     item + src + r * C * 2 + col * 16, true);
+            } else {
+                const int j = i - kTris * C * 4;
+                cp16(sh + lay.vec + j * 16, item + DeltaItem::kVec + j * 16, true);
+            }
+        }
+    }
+}
+
+// Rows p and p + 8 of a float32 P x N matrix as accumulators, `m` at (row p, this lane's column).
+template <int N> __device__ __forceinline__ void load_acc(const float *m, float (&S)[N / 8][4])
+{
+#pragma unroll
+    for (int n = 0; n < N / 8; ++n) {
+        const float2 u = *reinterpret_cast<const float2 *>(m + n * 8);
+        const float2 v = *reinterpret_cast<const float2 *>(m + 8 * N + n * 8);
+        S[n][0] = u.x; S[n][1] = u.y; S[n][2] = v.x; S[n][3] = v.y;
+    }
+}
+template <int N> __device__ __forceinline__ void store_acc(float *m, const float (&S)[N / 8][4])
+{
+#pragma unroll
+    for (int n = 0; n < N / 8; ++n) {
+        *reinterpret_cast<float2 *>(m + n * 8) = make_float2(S[n][0], S[n][1]);
+        *reinterpret_cast<float2 *>(m + 8 * N + n * 8) = make_float2(S[n][2], S[n][3]);
+    }
+}
+
+// Writes a 16 x 32 accumulator (rows p, columns tokens) rounded to bf16 as 32 rows of 16 values,
+// through this warp's columns of a tile that nobody reads any more.
+__device__ __forceinline__ void store_tokens(const float (&O)[4][4], uint32_t tile, int pitch,
+                                             uint32_t frag, bf16 *to, int64_t stride, int len,
+                                             int lane)
+{
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        uint32_t fo[4];
+        round_a(O[2 * n], O[2 * n + 1], fo);
+        stsm4_trans(frag + n * 16 * pitch, fo);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = lane; i < C * 2; i += 32) {   // 32 bytes of a row: two lanes
+        const int r = i / 2, half = i % 2;
+        if (r < len) {
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(tile + r * pitch + half * 16) : "memory");
+            *reinterpret_cast<uint4 *>(to + (int64_t)r * stride + half * 8) = v;
+        }
+    }
+}
+
+// Sums v[i] over the eight lanes of equal lane % 4, i = dot * 8 + (token tile) * 2 + e for kDots
+// dots; afterwards lane l has, in v[0] and v[1] (e), the sums of token tile (l >> 2) & 3, and of
+// dot l >> 4 for two dots (one dot: v[0] holds e = l >> 4).
+template <int kDots> __device__ __forceinline__ void fold_tokens(float (&v)[kDots * 8], int lane)
+{
+    if constexpr (kDots == 2) {
+#pragma unroll
+        for (int n = 8, o = 16; n > 1; n >>= 1, o >>= 1) {
+            const bool up = lane & o;
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const float mine = up ? v[n + i] : v[i], other = up ? v[i] : v[n + i];
+                v[i] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int n = 4, o = 8; n > 1; n >>= 1, o >>= 1) {
+            const bool up = lane & o;
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const float mine = up ? v[n + i] : v[i], other = up ? v[i] : v[n + i];
+                v[i] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+            }
+        }
+        const bool up = lane & 16;
+        const float mine = up ? v[1] : v[0], other = up ? v[0] : v[1];
+        v[0] = mine + __shfl_xor_sync(0xffffffffu, other, 16);
+    }
+}
+
 // A CTA has `heads` heads of one group and of each `rows` rows p: heads * rows / 16 warps.
-// grid: (sequences * H / heads * P / rows)
-template <int N>
+// grid: (sequences * H / heads * P / rows).  kBwd: the forward once more for the backward, which
+// keeps the state every 64 tokens, W, and the dot products of o and its gradient instead of o.
+template <int N, bool kBwd>
 __global__ void __launch_bounds__(256)
-delta_chain_kernel(const DeltaArgs a, const char *items, int64_t nchunks, const int2 *tab,
-                   const int32_t *cstart, const int *status, int heads, int rows)
+delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64_t nchunks,
+                   const int2 *tab, const int32_t *cstart, const int *status, int heads, int rows)
 {
     extern __shared__ __align__(128) char smem[];
     if (status && *status) return;
     constexpr int NT = N / 8;
     const int P = a.P;
-    const ChainStage lay(rows, N, heads);
+    const ChainStage lay(rows, N, heads, kBwd);
+    const ChainSlice slice(a, heads, rows, cstart != nullptr);
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const int splits = P / rows, blocks = a.H / heads * splits;
-    const int pb = (int)(blockIdx.x % splits) * rows;            // the CTA's first row
     const int hl = warp / (rows / 16), pl = warp % (rows / 16) * 16;   // this warp's head, rows
-    const int p0 = pb + pl;
-    const int h0 = (int)(blockIdx.x % blocks) / splits * heads;
-    const int64_t seq = blockIdx.x / blocks;
-    const int h = h0 + hl, g = h0 / (a.H / a.G);
-    const int64_t b = cstart ? 0 : seq;
+    const int p0 = slice.pb + pl, h = slice.h0 + hl;
+    const int64_t b = slice.b, seq = slice.seq;
     const int64_t c_begin = cstart ? cstart[seq] : 0, c_end = cstart ? cstart[seq + 1] : nchunks;
 
-    float S[NT][4];
-    const int64_t srow = ((seq * a.H + h) * P + p0 + lane / 4) * N + lane % 4 * 2;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        float2 u = make_float2(0.f, 0.f), v = u;
-        if (a.init) {
-            u = *reinterpret_cast<const float2 *>(a.init + srow + n * 8);
-            v = *reinterpret_cast<const float2 *>(a.init + srow + 8 * N + n * 8);
-        }
-        S[n][0] = u.x; S[n][1] = u.y; S[n][2] = v.x; S[n][3] = v.y;
-    }
+    float S[NT][4] = {};
+    const int64_t pn = (int64_t)(p0 + lane / 4) * N + lane % 4 * 2;   // this lane, in a P x N state
+    const int64_t srow = (seq * a.H + h) * P * N + pn;
+    if (a.init) load_acc<N>(a.init + srow, S);
 
     const uint32_t base = smem_u32(smem);
     auto load = [&](int64_t c, int stage) {
-        int64_t t0;
-        int len;
-        chunk_span(tab, c, C, a.L, t0, len);
-        const int64_t row0 = b * a.L + t0;
-        const uint32_t s = base + stage * lay.total;
-        const int nthr = blockDim.x;
-        const bf16 *kg = static_cast<const bf16 *>(a.k) + (row0 * a.G + g) * N;
-        const bf16 *qg = static_cast<const bf16 *>(a.q) + (row0 * a.G + g) * N;
-        for (int i = tid; i < C * (N / 8); i += nthr) {
-            const int r = i / (N / 8), col = i % (N / 8);
-            const bool on = r < len;
-            const int64_t off = on ? (int64_t)r * a.G * N + col * 8 : 0;
-            cp16(s + r * lay.kpitch + col * 16, kg + off, on);
-            cp16(s + (C + r) * lay.kpitch + col * 16, qg + off, on);
-        }
-        for (int x = 0; x < heads; ++x) {
-            const uint32_t sh = s + 2 * C * lay.kpitch + x * lay.head;
-            const bf16 *vg = static_cast<const bf16 *>(a.v) + (row0 * a.H + h0 + x) * P + pb;
-            const int pieces = rows / 8;
-            for (int i = tid; i < C * pieces; i += nthr) {
-                const int r = i / pieces, col = i % pieces;
-                const bool on = r < len;
-                cp16(sh + r * lay.vpitch + col * 16,
-                     vg + (on ? (int64_t)r * a.H * P + col * 8 : 0), on);
-            }
-            const char *item =
-                items + ((b * nchunks + c) * a.H + h0 + x) * DeltaItem::bytes(false);
-            const uint32_t tri = sh + C * lay.vpitch;
-            for (int i = tid; i < 3 * C * 4 + 32; i += nthr) {
-                if (i < 3 * C * 4) {   // Inv's two parts, Att: rows of four 16-byte pieces
-                    const int m = i / (C * 4), r = i / 4 % C, col = i % 4;
-                    const int src = (m == 2 ? DeltaItem::kAttHi : m * DeltaItem::kTri);
-                    cp16(tri + m * ChainStage::kTri + r * ChainStage::kTriPitch + col * 16,
-                         item + src + r * C * 2 + col * 16, true);
-                } else {
-                    const int j = i - 3 * C * 4;
-                    cp16(tri + 3 * ChainStage::kTri + j * 16, item + DeltaItem::kVec + j * 16,
-                         true);
-                }
-            }
-        }
+        load_stage<N, kBwd>(a, lay, slice, items, w.dout, nchunks, tab, c,
+                            base + stage * lay.total);
     };
 
     if (c_begin < c_end) load(c_begin, 0);
@@ -310,10 +403,12 @@ delta_chain_kernel(const DeltaArgs a, const char *items, int64_t nchunks, const 
 
         const uint32_t ks = base + stage * lay.total, qs = ks + C * lay.kpitch;
         const uint32_t vs = qs + C * lay.kpitch + hl * lay.head;
-        const uint32_t inv = vs + C * lay.vpitch, att = inv + 2 * ChainStage::kTri;
+        const uint32_t inv = vs + lay.tri, att = inv + 2 * ChainStage::kTri;
         const float *vec = reinterpret_cast<const float *>(
-            smem + stage * lay.total + 2 * C * lay.kpitch + hl * lay.head + C * lay.vpitch +
-            3 * ChainStage::kTri);
+            smem + stage * lay.total + 2 * C * lay.kpitch + hl * lay.head + lay.vec);
+        const int64_t item = (b * nchunks + c) * a.H + h;
+        if (kBwd && c % 2 == 0)
+            store_acc<N>(w.states + ((b * (w.n64 + 1) + c / 2) * a.H + h) * P * N + pn, S);
 
         // S K^T and S Q^T (columns: tokens)
         float X[4][4] = {}, O[4][4] = {};
@@ -331,6 +426,10 @@ delta_chain_kernel(const DeltaArgs a, const char *items, int64_t nchunks, const 
                 ldsm4(fb, qs + (n * 16 + row_nn) * lay.kpitch + s * 32 + col_nn);
                 mma_16816(O[2 * n], hi, fb[0], fb[1]);
                 mma_16816(O[2 * n + 1], hi, fb[2], fb[3]);
+                if (kBwd) {
+                    mma_16816(O[2 * n], lo, fb[0], fb[1]);
+                    mma_16816(O[2 * n + 1], lo, fb[2], fb[3]);
+                }
             }
         }
         // R = V - e K S^T, in place of S K^T; the output's part from the state takes its factor
@@ -381,18 +480,55 @@ delta_chain_kernel(const DeltaArgs a, const char *items, int64_t nchunks, const 
         }
         // O += Att W
         {
-            uint32_t hi[2][4];
-            round_a(W[0], W[1], hi[0]);
-            round_a(W[2], W[3], hi[1]);
+            uint32_t hi[2][4], lo[2][4];
+            split_a(W[0], W[1], hi[0], lo[0]);
+            split_a(W[2], W[3], hi[1], lo[1]);
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int s = 0; s <= n; ++s) {
-                    uint32_t fb[4];
-                    ldsm4(fb, att + (n * 16 + row_nn) * ChainStage::kTriPitch + s * 32 + col_nn);
-                    mma_16816(O[2 * n], hi[s], fb[0], fb[1]);
-                    mma_16816(O[2 * n + 1], hi[s], fb[2], fb[3]);
+                    uint32_t fb[4], fl[4];
+                    const uint32_t at =
+                        att + (n * 16 + row_nn) * ChainStage::kTriPitch + s * 32 + col_nn;
+                    ldsm4(fb, at);
+                    if (kBwd) ldsm4(fl, at + ChainStage::kTri);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        mma_16816(O[2 * n + m], hi[s], fb[2 * m], fb[2 * m + 1]);
+                        if (kBwd) {
+                            mma_16816(O[2 * n + m], lo[s], fb[2 * m], fb[2 * m + 1]);
+                            mma_16816(O[2 * n + m], hi[s], fl[2 * m], fl[2 * m + 1]);
+                        }
+                    }
                 }
+        }
+        int64_t t0;
+        int len;
+        chunk_span(tab, c, C, a.L, t0, len);
+        const int64_t tokens = ((b * a.L + t0) * a.H + h) * P + p0;   // this warp's rows of v, o
+        if constexpr (kBwd) {
+            float d[8];   // <dO, O> over this warp's rows, per token
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                uint32_t fd[4];
+                ldsm4_trans(fd, vaddr + (C + n * 16) * lay.vpitch);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const int t = 2 * n + m;
+                    d[2 * t] = fmaf(bf16_lo(fd[2 * m]), O[t][0], bf16_lo(fd[2 * m + 1]) * O[t][2]);
+                    d[2 * t + 1] =
+                        fmaf(bf16_hi(fd[2 * m]), O[t][1], bf16_hi(fd[2 * m + 1]) * O[t][3]);
+                }
+            }
+            fold_tokens<1>(d, lane);
+            const int64_t tile = item * (P / 16) + p0 / 16;
+            w.dot_oo[tile * C + (lane >> 2 & 3) * 8 + lane % 4 * 2 + (lane >> 4)] = d[0];
+            float4 *wf = reinterpret_cast<float4 *>(w.wfrag + tile * (16 * C)) + lane;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                wf[t * 32] = make_float4(W[t][0], W[t][1], W[t][2], W[t][3]);
+            store_tokens(W, vs + pl * 2, lay.vpitch, vaddr, w.w + tokens, (int64_t)a.H * P, len,
+                         lane);
         }
         // S = E S + (E / e beta W)^T K
         const float E = vec[3 * C];
@@ -419,40 +555,236 @@ delta_chain_kernel(const DeltaArgs a, const char *items, int64_t nchunks, const 
                 mma_16816(S[2 * n + 1], lo, fb[2], fb[3]);
             }
         }
-        // the output through this warp's columns of the V tile, which nobody reads any more
+        if constexpr (!kBwd)
+            store_tokens(O, vs + pl * 2, lay.vpitch, vaddr, static_cast<bf16 *>(a.o) + tokens,
+                         (int64_t)a.H * P, len, lane);
+    }
+    cp_wait<0>();
+    if (kBwd)
+        store_acc<N>(w.states + ((b * (w.n64 + 1) + w.n64) * a.H + h) * P * N + pn, S);
+    else if (a.final_state)
+        store_acc<N>(a.final_state + srow, S);
+}
+
+// The adjoint recurrence, chunk by chunk from the end, in the same layout (dS in registers, rows p
+// per warp).  With Y = beta dL/dU, the gradient of the written values:
+//
+//     Y  = Att^T dO + sw K dS'^T,    dV = Inv^T Y,
+//     dS = E dS' + (eq dO)^T Q - (ek dV)^T K
+//
+// sw, ek and eq are the factors of the forward (decays, norms, beta, scale).  It writes dV, the dot
+// products of each token's dV with V and W, every 64 tokens dS' (bf16) and <dS', S'>, and dS of
+// the initial state.
+template <int N>
+__global__ void __launch_bounds__(256)
+delta_adjoint_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64_t nchunks,
+                     int heads, int rows)
+{
+    extern __shared__ __align__(128) char smem[];
+    constexpr int NT = N / 8;
+    const int P = a.P;
+    const ChainStage lay(rows, N, heads, true);
+    const ChainSlice slice(a, heads, rows, false);
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int hl = warp / (rows / 16), pl = warp % (rows / 16) * 16;
+    const int p0 = slice.pb + pl, h = slice.h0 + hl;
+    const int64_t b = slice.b;
+
+    float D[NT][4] = {};
+    const int64_t pn = (int64_t)(p0 + lane / 4) * N + lane % 4 * 2;
+    const int64_t srow = (b * a.H + h) * P * N + pn;
+    if (w.dfinal) load_acc<N>(w.dfinal + srow, D);
+
+    const uint32_t base = smem_u32(smem);
+    auto load = [&](int64_t c, int stage) {
+        load_stage<N, true>(a, lay, slice, items, w.dout, nchunks, nullptr, c,
+                            base + stage * lay.total);
+    };
+    load(nchunks - 1, 0);
+    cp_commit();
+    const int row_nn = lane % 8 + lane / 16 * 8, col_nn = (lane / 8 & 1) * 16;   // rows on n
+    const int row_kk = lane % 8 + (lane / 8 & 1) * 8, col_kk = lane / 16 * 16;   // rows on k
+    for (int64_t c = nchunks - 1; c >= 0; --c) {
+        const int stage = (int)(nchunks - 1 - c) & 1;
+        cp_wait<0>();
+        __syncthreads();
+        if (c > 0) load(c - 1, stage ^ 1);
+        cp_commit();
+
+        const uint32_t ks = base + stage * lay.total, qs = ks + C * lay.kpitch;
+        const uint32_t vs = qs + C * lay.kpitch + hl * lay.head;
+        const uint32_t inv = vs + lay.tri, att = inv + 2 * ChainStage::kTri;
+        const float *vec = reinterpret_cast<const float *>(
+            smem + stage * lay.total + 2 * C * lay.kpitch + hl * lay.head + lay.vec);
+        const int64_t item = (b * nchunks + c) * a.H + h;
+        const int64_t tile = item * (P / 16) + p0 / 16;
+        float4 wf[4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            uint32_t fo[4];
-            round_a(O[2 * n], O[2 * n + 1], fo);
-            stsm4_trans(vaddr + n * 16 * lay.vpitch, fo);
+        for (int t = 0; t < 4; ++t)
+            wf[t] = reinterpret_cast<const float4 *>(w.wfrag + tile * (16 * C))[t * 32 + lane];
+
+        if (c % 2 == 1 || c == nchunks - 1) {   // the end of a span of 64 tokens
+            const int64_t span = (b * w.n64 + c / 2) * a.H + h;
+            const float *sn = w.states + ((b * (w.n64 + 1) + c / 2 + 1) * a.H + h) * P * N + pn;
+            bf16 *ds = w.dstates + span * P * N + pn;
+            float f = 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float2 u = *reinterpret_cast<const float2 *>(sn + n * 8);
+                const float2 v = *reinterpret_cast<const float2 *>(sn + 8 * N + n * 8);
+                f = fmaf(D[n][0], u.x, fmaf(D[n][1], u.y, fmaf(D[n][2], v.x, fmaf(D[n][3], v.y, f))));
+                *reinterpret_cast<uint32_t *>(ds + n * 8) = pack_bf16x2(D[n][0], D[n][1]);
+                *reinterpret_cast<uint32_t *>(ds + 8 * N + n * 8) = pack_bf16x2(D[n][2], D[n][3]);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+            if (lane == 0) w.dot_ss[span * (P / 16) + p0 / 16] = f;
         }
-        __syncwarp();
+
+        // dS' K^T (columns: tokens)
+        float Y[4][4] = {};
+#pragma unroll
+        for (int s = 0; s < N / 16; ++s) {
+            uint32_t hi[4], lo[4], fb[4];
+            split_a(D[2 * s], D[2 * s + 1], hi, lo);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                ldsm4(fb, ks + (n * 16 + row_nn) * lay.kpitch + s * 32 + col_nn);
+                mma_16816(Y[2 * n], hi, fb[0], fb[1]);
+                mma_16816(Y[2 * n + 1], hi, fb[2], fb[3]);
+                mma_16816(Y[2 * n], lo, fb[0], fb[1]);
+                mma_16816(Y[2 * n + 1], lo, fb[2], fb[3]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const float2 sw = *reinterpret_cast<const float2 *>(vec + C + t * 8 + lane % 4 * 2);
+            Y[t][0] *= sw.x; Y[t][1] *= sw.y; Y[t][2] *= sw.x; Y[t][3] *= sw.y;
+        }
+        // Y += dO^T Att: blocks of 16 tokens on and below Att's diagonal.  dO^T, read transposed,
+        // is an A operand as it is.
+        const uint32_t vaddr = vs + pl * 2 + row_nn * lay.vpitch + col_nn;
+        const uint32_t daddr = vaddr + C * lay.vpitch;
+        uint32_t fd[2][4];
+        ldsm4_trans(fd[0], daddr);
+        ldsm4_trans(fd[1], daddr + 16 * lay.vpitch);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int n = 0; n <= s; ++n) {
+                uint32_t fh[4], fl[4];
+                const uint32_t at =
+                    att + (s * 16 + row_kk) * ChainStage::kTriPitch + n * 32 + col_kk;
+                ldsm4_trans(fh, at);
+                ldsm4_trans(fl, at + ChainStage::kTri);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    mma_16816(Y[2 * n + m], fd[s], fh[2 * m], fh[2 * m + 1]);
+                    mma_16816(Y[2 * n + m], fd[s], fl[2 * m], fl[2 * m + 1]);
+                }
+            }
+        // dV = Y + (Inv - I)^T Y
+        float V[4][4];
+        {
+            uint32_t hi[2][4], lo[2][4];
+            split_a(Y[0], Y[1], hi[0], lo[0]);
+            split_a(Y[2], Y[3], hi[1], lo[1]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) V[t][r] = Y[t][r];
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int n = 0; n <= s; ++n) {
+                    uint32_t fh[4], fl[4];
+                    const uint32_t at =
+                        inv + (s * 16 + row_kk) * ChainStage::kTriPitch + n * 32 + col_kk;
+                    ldsm4_trans(fh, at);
+                    ldsm4_trans(fl, at + ChainStage::kTri);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        mma_16816(V[2 * n + m], hi[s], fh[2 * m], fh[2 * m + 1]);
+                        mma_16816(V[2 * n + m], lo[s], fh[2 * m], fh[2 * m + 1]);
+                        mma_16816(V[2 * n + m], hi[s], fl[2 * m], fl[2 * m + 1]);
+                    }
+                }
+        }
+        // per token: <dV, V> and <dV, W> over this warp's rows
+        {
+            float d[16];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                uint32_t fv[4];
+                ldsm4_trans(fv, vaddr + n * 16 * lay.vpitch);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const int t = 2 * n + m;
+                    d[2 * t] = fmaf(bf16_lo(fv[2 * m]), V[t][0], bf16_lo(fv[2 * m + 1]) * V[t][2]);
+                    d[2 * t + 1] =
+                        fmaf(bf16_hi(fv[2 * m]), V[t][1], bf16_hi(fv[2 * m + 1]) * V[t][3]);
+                    d[8 + 2 * t] = fmaf(wf[t].x, V[t][0], wf[t].z * V[t][2]);
+                    d[8 + 2 * t + 1] = fmaf(wf[t].y, V[t][1], wf[t].w * V[t][3]);
+                }
+            }
+            fold_tokens<2>(d, lane);
+            float *to = (lane & 16 ? w.dot_vw : w.dot_vv) + tile * C;
+            *reinterpret_cast<float2 *>(to + (lane >> 2 & 3) * 8 + lane % 4 * 2) =
+                make_float2(d[0], d[1]);
+        }
         int64_t t0;
         int len;
-        chunk_span(tab, c, C, a.L, t0, len);
-        bf16 *og = static_cast<bf16 *>(a.o) + ((b * a.L + t0) * a.H + h) * P + p0;
+        chunk_span(nullptr, c, C, a.L, t0, len);
+        store_tokens(V, vs + pl * 2, lay.vpitch, vaddr,
+                     w.dv + ((b * a.L + t0) * a.H + h) * P + p0, (int64_t)a.H * P, len, lane);
+
+        // dS = E dS' + (eq dO)^T Q - (ek dV)^T K
+        const float E = vec[3 * C];
 #pragma unroll
-        for (int i = lane; i < C * 2; i += 32) {   // 32 bytes of a row: two lanes
-            const int r = i / 2, half = i % 2;
-            if (r < len) {
-                uint4 v;
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                             : "r"(vs + pl * 2 + r * lay.vpitch + half * 16) : "memory");
-                *reinterpret_cast<uint4 *>(og + (int64_t)r * a.H * P + half * 8) = v;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) D[n][r] *= E;
+        float Z[4][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const float2 ek = *reinterpret_cast<const float2 *>(vec + t * 8 + lane % 4 * 2);
+            const float2 eq = *reinterpret_cast<const float2 *>(vec + 2 * C + t * 8 + lane % 4 * 2);
+            const uint32_t x = fd[t / 2][t % 2 * 2], y = fd[t / 2][t % 2 * 2 + 1];
+            Z[t][0] = eq.x * bf16_lo(x); Z[t][1] = eq.y * bf16_hi(x);
+            Z[t][2] = eq.x * bf16_lo(y); Z[t][3] = eq.y * bf16_hi(y);
+            V[t][0] *= -ek.x; V[t][1] *= -ek.y; V[t][2] *= -ek.x; V[t][3] *= -ek.y;
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            uint32_t zh[4], zl[4], vh[4], vl[4];
+            split_a(Z[2 * s], Z[2 * s + 1], zh, zl);
+            split_a(V[2 * s], V[2 * s + 1], vh, vl);
+            const uint32_t at = (s * 16 + row_kk) * lay.kpitch + col_kk;
+#pragma unroll
+            for (int n = 0; n < NT / 2; ++n) {
+                uint32_t fq[4], fk[4];
+                ldsm4_trans(fq, qs + at + n * 32);
+                ldsm4_trans(fk, ks + at + n * 32);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    mma_16816(D[2 * n + m], zh, fq[2 * m], fq[2 * m + 1]);
+                    mma_16816(D[2 * n + m], vh, fk[2 * m], fk[2 * m + 1]);
+                    mma_16816(D[2 * n + m], zl, fq[2 * m], fq[2 * m + 1]);
+                    mma_16816(D[2 * n + m], vl, fk[2 * m], fk[2 * m + 1]);
+                }
             }
         }
     }
     cp_wait<0>();
-    if (a.final_state) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            *reinterpret_cast<float2 *>(a.final_state + srow + n * 8) =
-                make_float2(S[n][0], S[n][1]);
-            *reinterpret_cast<float2 *>(a.final_state + srow + 8 * N + n * 8) =
-                make_float2(S[n][2], S[n][3]);
-        }
-    }
+    if (w.dinit) store_acc<N>(w.dinit + srow, D);
+}
+
+// Rows of a head per CTA: all of them, or fewer where the launch would leave SMs empty.
+int chain_rows(const DeltaArgs &a, int64_t nseq)
+{
+    int rows = a.P;
+    while (nseq * a.H * (a.P / rows) < 148 && rows % 32 == 0) rows /= 2;
+    return rows;
 }
 
 }  // namespace
@@ -478,24 +810,40 @@ cudaError_t launch_delta_prep(const DeltaArgs &a, char *items, bool for_backward
     return cudaGetLastError();
 }
 
-cudaError_t launch_delta_chain(const DeltaArgs &a, const char *items, int64_t nchunks,
-                               const int2 *tab, const int32_t *cstart, const int *status,
-                               cudaStream_t st)
+cudaError_t launch_delta_chain(const DeltaArgs &a, const DeltaBwd *bwd, const char *items,
+                               int64_t nchunks, const int2 *tab, const int32_t *cstart,
+                               const int *status, cudaStream_t st)
 {
     const int64_t nseq = cstart ? a.nseq : a.batch;
-    int heads = 1, rows = a.P;
-    while (nseq * a.H * (a.P / rows) < 148 && rows % 32 == 0) rows /= 2;
+    const int heads = 1, rows = chain_rows(a, nseq);
     const unsigned grid = (unsigned)(nseq * (a.H / heads) * (a.P / rows));
     const unsigned threads = (unsigned)(heads * rows / 16 * 32);
-    const int smem = 2 * ChainStage(rows, a.N, heads).total;
+    const int smem = 2 * ChainStage(rows, a.N, heads, bwd != nullptr).total;
+    const DeltaBwd w = bwd ? *bwd : DeltaBwd{};
     auto go = [&](auto kern) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        kern<<<grid, threads, smem, st>>>(a, items, nchunks, tab, cstart, status, heads,
-                                           rows);
+        kern<<<grid, threads, smem, st>>>(a, w, items, nchunks, tab, cstart, status, heads, rows);
         return cudaGetLastError();
     };
-    return a.N == 128 ? go(delta_chain_kernel<128>) : go(delta_chain_kernel<64>);
+    if (bwd) return a.N == 128 ? go(delta_chain_kernel<128, true>) : go(delta_chain_kernel<64, true>);
+    return a.N == 128 ? go(delta_chain_kernel<128, false>) : go(delta_chain_kernel<64, false>);
+}
+
+cudaError_t launch_delta_adjoint(const DeltaArgs &a, const DeltaBwd &w, const char *items,
+                                 int64_t nchunks, cudaStream_t st)
+{
+    const int heads = 1, rows = chain_rows(a, a.batch);
+    const unsigned grid = (unsigned)(a.batch * (a.H / heads) * (a.P / rows));
+    const unsigned threads = (unsigned)(heads * rows / 16 * 32);
+    const int smem = 2 * ChainStage(rows, a.N, heads, true).total;
+    auto go = [&](auto kern) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        kern<<<grid, threads, smem, st>>>(a, w, items, nchunks, heads, rows);
+        return cudaGetLastError();
+    };
+    return a.N == 128 ? go(delta_adjoint_kernel<128>) : go(delta_adjoint_kernel<64>);
 }
 
 }  // namespace ssd

@@ -13,6 +13,7 @@ stands in front of and behind either mixer:
 
     o, final = delta_rule_fwd(q, k, v, g, beta, qk_l2norm=True)
     o, finals = delta_rule_varlen_fwd(q, k, v, g, beta, cu_seqlens)
+    grads = delta_rule_bwd(q, k, v, g, beta, dout)
     o = delta_rule_update(state, q, k, v, g, beta)      # one token, state updated in place
     y, h = rms_norm(x, weight, residual=residual)
     y8, scales = rms_norm(x, weight, z=z, gate="pre", quant_group=128)
@@ -138,6 +139,12 @@ def lib():
     L.ssd_delta_rule_varlen_fwd.argtypes = [ctypes.POINTER(Shape), _vp, _vp, _vp, _vp, _vp,
                                             ctypes.POINTER(DeltaOptions), _vp, ctypes.c_int, _vp,
                                             _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    L.ssd_delta_rule_bwd_workspace_size.restype = ctypes.c_size_t
+    L.ssd_delta_rule_bwd_workspace_size.argtypes = [ctypes.POINTER(Shape)]
+    L.ssd_delta_rule_bwd.restype = ctypes.c_int
+    L.ssd_delta_rule_bwd.argtypes = [ctypes.POINTER(Shape), _vp, _vp, _vp, _vp, _vp,
+                                     ctypes.POINTER(DeltaOptions), _vp, _vp, _vp, _vp, _vp, _vp,
+                                     _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
     L.ssd_delta_rule_update.restype = ctypes.c_int
     L.ssd_delta_rule_update.argtypes = [ctypes.POINTER(Shape), _vp, _vp, _vp, _vp, _vp, _vp,
                                         ctypes.POINTER(DeltaOptions), _vp, _vp]
@@ -655,6 +662,35 @@ def delta_rule_varlen_fwd(q, k, v, g, beta, cu_seqlens, scale=None, init_states=
              ctypes.byref(_delta_options(scale, shape.dstate, qk_l2norm)), _ptr(cu_seqlens), nseq,
              _ptr(init_states), _ptr(o), _ptr(final_states), _ptr(workspace), workspace.numel())
     return o, final_states
+
+
+def delta_rule_bwd(q, k, v, g, beta, dout, scale=None, init_state=None, dfinal=None,
+                   qk_l2norm: bool = False, return_dinit: bool = True, workspace=None,
+                   stream=None):
+    """Gradients of delta_rule_fwd (ssd_delta_rule_bwd), given dout (like o) and dfinal
+    (b, H, P, N) float32 or None: a dict of dq, dk, dv (bf16, like q, k, v), dg (None without g)
+    and dbeta (b, L, H) float32, dinit (b, H, P, N) float32 (None unless return_dinit)."""
+    torch = _torch()
+    shape = _delta_inputs(q, k, v, g, beta, None, ((init_state, "init_state"),
+                                                   (dfinal, "dfinal")))
+    _on(dout, "dout", v.shape, v.dtype, v.device)
+    call = _Call(v, stream)
+    n = lib().ssd_delta_rule_bwd_workspace_size(ctypes.byref(shape))
+    if n == 0:
+        raise SSDError(SSD_ERR_UNSUPPORTED, last_error())
+    out = {"d" + name: call.empty(t.shape, t.dtype)
+           for name, t in (("q", q), ("k", k), ("v", v))}
+    out["dg"] = None if g is None else call.empty(g.shape, torch.float32)
+    out["dbeta"] = call.empty(beta.shape, torch.float32)
+    out["dinit"] = call.empty((shape.batch, shape.nheads, shape.headdim, shape.dstate),
+                              torch.float32) if return_dinit else None
+    workspace = call.workspace(workspace, n)
+    call.run(lib().ssd_delta_rule_bwd, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+             _ptr(beta), ctypes.byref(_delta_options(scale, shape.dstate, qk_l2norm)),
+             _ptr(init_state), _ptr(dout), _ptr(dfinal), _ptr(out["dq"]), _ptr(out["dk"]),
+             _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dbeta"]), _ptr(out["dinit"]),
+             _ptr(workspace), workspace.numel())
+    return out
 
 
 def delta_rule_update(state, q, k, v, g, beta, scale=None, qk_l2norm: bool = False, o=None,
