@@ -45,7 +45,8 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
+    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "--threads", "0", "-shared",
+           "-Xcompiler", "-fPIC",
            "-I", os.path.join(ROOT, "include"), "-o", tmp, *sources()]
     if verbose_ptxas:
         cmd[1:1] = ["-Xptxas", "-v"]

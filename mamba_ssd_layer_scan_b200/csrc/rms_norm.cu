@@ -12,9 +12,12 @@
 // HBM-bound: each row is read once into registers, reduced once -- sum(h^2) together with the
 // row's largest |h w| (forward, one scale per row) or with sum(dn w h) (backward) -- and written.
 // A row of up to 32 vectors belongs to 8, 16 or 32 lanes of a warp, a longer one to a whole CTA;
-// the CTAs walk the rows with their slice of w in registers.
+// the CTAs walk the rows with their slice of w in registers and the next rows on their way.
+#include <algorithm>
+
 #include "api.cuh"
 #include "common.cuh"
+#include "delta_mma.cuh"
 
 namespace ssd {
 namespace {
@@ -22,10 +25,14 @@ namespace {
 constexpr int kRowThreads = 256;   // CTA of the lanes-per-row variants
 constexpr int kMaxDim = 16384;
 constexpr int kMaxRowThreads = 512;
-constexpr int kBwdCtas = 592;      // most CTAs of the backward: four per SM, each with a row of
-                                   // partial weight gradients
+constexpr int kBwdCtas = 608;      // most CTAs of the backward: four per SM, each with a row of
+                                   // partial weight gradients (a multiple of 32)
 constexpr float kE4m3Max = 448.f;
 constexpr float kMinScale = 1e-30f;
+
+// What a launch computes besides the norm: the kernels' variants.
+enum : int { kPlain, kResidual, kPre, kPost };
+enum : int { kNoQuant, kPerRow, kPerGroup };
 
 struct NormArgs {
     const void *x, *residual, *z, *dy, *dres;
@@ -79,11 +86,6 @@ template <> struct __align__(16) Pack<bf16, 8> {
 };
 
 template <typename T, int VEC>
-__device__ __forceinline__ void load(const void *base, int64_t at, float (&f)[VEC])
-{
-    reinterpret_cast<const Pack<T, VEC> *>(static_cast<const T *>(base) + at)->get(f);
-}
-template <typename T, int VEC>
 __device__ __forceinline__ void store(void *base, int64_t at, const float (&f)[VEC])
 {
     Pack<T, VEC> p;
@@ -133,7 +135,72 @@ template <int VEC> __device__ __forceinline__ void store_e4m3(uint8_t *to, const
     }
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// 1 / (1 + 2^(-z log2(e))), each step to about 2^-22; far from 0 exactly 0 or 1.
+__device__ __forceinline__ float sigmoid(float z)
+{
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * z));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
+
+// Two float32 operations in one instruction: x <- x y, and d + x y.
+__device__ __forceinline__ uint64_t pair(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float &x, float &y)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t d)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(d));
+    return r;
+}
+// x <- x y for a thread's vector (y: another vector, or one factor), and the two halves of the sum
+// of squares.
+template <int VEC> __device__ __forceinline__ void times(float (&x)[VEC], const float (&y)[VEC])
+{
+    if constexpr (VEC == 1) x[0] *= y[0];
+    else
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2)
+            unpair(mul2(pair(x[i], x[i + 1]), pair(y[i], y[i + 1])), x[i], x[i + 1]);
+}
+template <int VEC> __device__ __forceinline__ void times(float (&x)[VEC], float f)
+{
+    if constexpr (VEC == 1) x[0] *= f;
+    else
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2)
+            unpair(mul2(pair(x[i], x[i + 1]), pair(f, f)), x[i], x[i + 1]);
+}
+template <int VEC>
+__device__ __forceinline__ void add_products(uint64_t &sum, const float (&x)[VEC],
+                                             const float (&y)[VEC])
+{
+    if constexpr (VEC == 1) sum = fma2(pair(x[0], 0.f), pair(y[0], 0.f), sum);
+    else
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2)
+            sum = fma2(pair(x[i], x[i + 1]), pair(y[i], y[i + 1]), sum);
+}
+__device__ __forceinline__ float both(uint64_t p)
+{
+    float x, y;
+    unpair(p, x, y);
+    return x + y;
+}
 
 // Reduces a (a sum) and b (a sum, or a maximum when kMax) over the threads of a row.  TPR: lanes
 // per row, 0 for the whole CTA; `buf` alternates between two halves from row to row, so that one
@@ -148,255 +215,344 @@ __device__ __forceinline__ void reduce_row(float &a, float &b, float2 *red, int 
         const float other = __shfl_xor_sync(0xffffffffu, b, o);
         b = kMax ? max_nan(b, other) : b + other;
     }
-    if constexpr (TPR == 0) {
-        const int warps = blockDim.x / 32;
+    if constexpr (TPR == 0) {   // every warp reduces the warps' results (at most 16) again
+        const int warps = blockDim.x / 32, lane = threadIdx.x % 32;
         float2 *r = red + buf * (kMaxRowThreads / 32);
-        if (threadIdx.x % 32 == 0) r[threadIdx.x / 32] = make_float2(a, b);
+        if (lane == 0) r[threadIdx.x / 32] = make_float2(a, b);
         __syncthreads();
-        a = 0.f;
-        b = 0.f;
-        for (int i = 0; i < warps; ++i) {
-            const float2 v = r[i];
-            a += v.x;
-            b = kMax ? max_nan(b, v.y) : b + v.y;
+        const float2 v = lane % 16 < warps ? r[lane % 16] : make_float2(0.f, 0.f);
+        a = v.x;
+        b = v.y;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            const float other = __shfl_xor_sync(0xffffffffu, b, o);
+            b = kMax ? max_nan(b, other) : b + other;
         }
     }
 }
 
-template <int TPR> __device__ __forceinline__ int threads_per_row()
-{
-    return TPR == 0 ? (int)blockDim.x : TPR;
-}
+// How a CTA walks the rows, and this thread's share of a row: vectors j * threads + lane of VEC
+// elements, j < NV.  The operands' vectors of 16 bytes come some rows ahead through a ring in
+// shared memory (cp.async); a thread reads what it copied itself, so the ring needs no barrier.
+// With the next row in registers instead, 16384 x 2560 ran at 72 % (residual) and its backward
+// at 33 % of the copy bandwidth: too few warps fitted.
+__host__ __device__ constexpr int rows_ahead(int nv) { return nv == 1 ? 3 : nv == 2 ? 2 : 1; }
+template <typename T, int VEC, int NV, int TPR, int kOps> struct Walk {
+    static constexpr bool kRing = sizeof(T) * VEC == 16;
+    static constexpr int kAhead = rows_ahead(NV);
+    int tpr, lane, sub, dim;
+    int64_t row, step, rows;
+    bool on[NV];
+    uint32_t slot;   // this thread's first slot in the ring
+    int turn;
+    const void *op[kOps];
 
-// A thread's elements of its row: vectors j * threads + lane of VEC elements, j < NV.
-template <typename T, int VEC, int NV, int TPR>
+    __device__ __forceinline__ Walk(const NormArgs &a, char *ring) : dim(a.dim), rows(a.rows), turn(0)
+    {
+        tpr = TPR == 0 ? (int)blockDim.x : TPR;
+        lane = TPR == 0 ? threadIdx.x : threadIdx.x % tpr;
+        sub = TPR == 0 ? 0 : threadIdx.x / tpr;
+        const int per_cta = TPR == 0 ? 1 : kRowThreads / tpr;
+        step = (int64_t)gridDim.x * per_cta;
+        row = (int64_t)blockIdx.x * per_cta + sub;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) on[j] = (j * tpr + lane) * VEC < dim;
+        slot = sm100::smem_u32(ring) + threadIdx.x * 16;
+    }
+    __device__ __forceinline__ int64_t at(int j) const
+    {
+        return row * dim + (j * tpr + lane) * VEC;
+    }
+    __device__ __forceinline__ uint32_t place(int o, int j) const
+    {
+        return slot + ((turn * kOps + o) * NV + j) * blockDim.x * 16;
+    }
+    // copies of the row `ahead` turns on into the present turn's slots
+    __device__ __forceinline__ void prefetch(int ahead)
+    {
+        if constexpr (kRing) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                if (row + ahead * step >= rows || !on[j]) continue;
+#pragma unroll
+                for (int o = 0; o < kOps; ++o)
+                    cp16(place(o, j), static_cast<const T *>(op[o]) + at(j) + ahead * step * dim, true);
+            }
+            cp_commit();
+        }
+    }
+    __device__ __forceinline__ void start()
+    {
+        for (int i = 0; i < kAhead; ++i) {
+            prefetch(i);
+            turn = turn + 1 == kAhead ? 0 : turn + 1;
+        }
+    }
+    __device__ __forceinline__ void arrived() { if constexpr (kRing) cp_wait<kAhead - 1>(); }
+    // this thread's vector j of operand o
+    __device__ __forceinline__ Pack<T, VEC> get(int o, int j) const
+    {
+        Pack<T, VEC> p;
+        if constexpr (kRing) {
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(place(o, j)) : "memory");
+            memcpy(&p, &v, 16);
+        } else {
+            p = *reinterpret_cast<const Pack<T, VEC> *>(static_cast<const T *>(op[o]) + at(j));
+        }
+        return p;
+    }
+    // the next row; call it once this row's vectors have been used
+    __device__ __forceinline__ void next()
+    {
+        prefetch(kAhead);
+        turn = turn + 1 == kAhead ? 0 : turn + 1;
+        row += step;
+    }
+    // the CTA's rows; the last ones may lie behind the end for some threads, which then only take
+    // part in the reductions
+    __device__ __forceinline__ bool more() const { return row - sub < rows; }
+    __device__ __forceinline__ bool live() const { return row < rows; }
+};
+
+__host__ __device__ constexpr int norm_ops(int mode) { return mode == kPlain ? 1 : 2; }
+__host__ __device__ constexpr int norm_bwd_ops(int mode) { return mode == kPlain ? 2 : 3; }
+
+template <typename T, int VEC, int NV, int TPR, int kMode, int kQuant>
 __global__ void __launch_bounds__(TPR == 0 ? kMaxRowThreads : kRowThreads)
 rms_norm_kernel(const NormArgs a)
 {
     __shared__ float2 red[2 * (kMaxRowThreads / 32)];
-    const int tpr = threads_per_row<TPR>();
-    const int rows_per_cta = TPR == 0 ? 1 : kRowThreads / tpr;
-    const int lane = TPR == 0 ? threadIdx.x : threadIdx.x % tpr;
+    extern __shared__ __align__(16) char ring[];
     const int dim = a.dim;
     const float inv_dim = 1.f / (float)dim;
-    float w[NV][VEC];
-    bool on[NV];
+    Walk<T, VEC, NV, TPR, norm_ops(kMode)> w(a, ring);
+    w.op[0] = a.x;
+    if constexpr (kMode != kPlain) w.op[1] = kMode == kResidual ? a.residual : a.z;
+    w.start();
+    float wt[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int e = (j * tpr + lane) * VEC;
-        on[j] = e < dim;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) w[j][i] = 0.f;
-        if (on[j]) load_w<VEC>(a.w + e, w[j]);
+        for (int i = 0; i < VEC; ++i) wt[j][i] = 0.f;
+        if (w.on[j]) load_w<VEC>(a.w + (j * w.tpr + w.lane) * VEC, wt[j]);
     }
-    int buf = 0;
-    const int64_t step = (int64_t)gridDim.x * rows_per_cta;
-    const int64_t first = (int64_t)blockIdx.x * rows_per_cta;
-    const int sub = TPR == 0 ? 0 : threadIdx.x / tpr;
-    for (int64_t base = first; base < a.rows; base += step, buf ^= 1) {
-        const int64_t row = base + sub;
-        const bool live = row < a.rows;   // the others take part in the shuffles only
-        float h[NV][VEC], gate[NV][VEC];
-        float ss = 0.f, top = 0.f;
+    for (int buf = 0; w.more(); buf ^= 1) {
+        const bool live = w.live();
+        float h[NV][VEC];
+        float top = 0.f;
+        uint64_t sums = 0;
+        w.arrived();
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t at = row * dim + (j * tpr + lane) * VEC;
+            float other[VEC];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) h[j][i] = 0.f;
-            if (live && on[j]) {
-                load<T, VEC>(a.x, at, h[j]);
-                if (a.residual) {
-                    float r[VEC];
-                    load<T, VEC>(a.residual, at, r);
+            for (int i = 0; i < VEC; ++i) h[j][i] = other[i] = 0.f;
+            if (live && w.on[j]) {
+                w.get(0, j).get(h[j]);
+                if constexpr (kMode != kPlain) w.get(1, j).get(other);
+                if constexpr (kMode == kResidual) {
+                    Pack<T, VEC> sum;
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        h[j][i] = to_f32(from_f32<T>(h[j][i] + r[i]));
-                    store<T, VEC>(a.res_out, at, h[j]);
-                }
-                if (a.gate) {
-                    load<T, VEC>(a.z, at, gate[j]);
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        const float s = silu(gate[j][i]);
-                        if (a.gate == 1) h[j][i] *= s;
-                        else gate[j][i] = s;
-                    }
+                    for (int i = 0; i < VEC; ++i) h[j][i] += other[i];
+                    sum.set(h[j]);
+                    sum.get(h[j]);
+                    *reinterpret_cast<Pack<T, VEC> *>(static_cast<T *>(a.res_out) + w.at(j)) = sum;
                 }
             }
+            if constexpr (kMode == kPre || kMode == kPost) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                ss = fmaf(h[j][i], h[j][i], ss);
-                float v = h[j][i] * w[j][i];
-                if (a.gate == 2 && live && on[j]) v *= gate[j][i];
-                h[j][i] = v;
-                top = max_nan(top, fabsf(v));
+                for (int i = 0; i < VEC; ++i) other[i] *= sigmoid(other[i]);
+            }
+            if constexpr (kMode == kPre) times(h[j], other);
+            add_products(sums, h[j], h[j]);
+            times(h[j], wt[j]);
+            if constexpr (kMode == kPost) times(h[j], other);
+            if constexpr (kQuant == kPerRow) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) top = max_nan(top, fabsf(h[j][i]));
             }
         }
-        const bool per_row = a.quant == dim;
+        float ss = both(sums);
         reduce_row<TPR, true>(ss, top, red, buf);
         const float r = rsqrtf(fmaf(ss, inv_dim, a.eps));
-        float scale = fmaxf(top * r / kE4m3Max, kMinScale);
-        if (top != top) scale = top;
+        float scale = max_nan(top * r * (1.f / kE4m3Max), kMinScale);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int e = (j * tpr + lane) * VEC;
+            const int e = (j * w.tpr + w.lane) * VEC;
+            times(h[j], r);
+            if constexpr (kQuant != kNoQuant) {
+                if constexpr (kQuant == kPerGroup) {   // 32, 64 or 128 elements: their lanes
+                    float m = 0.f;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) h[j][i] *= r;
-            if (a.quant && !per_row) {   // one scale per `quant` elements: quant / VEC lanes
-                float m = 0.f;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) m = max_nan(m, fabsf(h[j][i]));
-                for (int o = a.quant / VEC / 2; o > 0; o >>= 1)
-                    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-                scale = fmaxf(m / kE4m3Max, kMinScale);
-                if (m != m) scale = m;
-            }
-            if (!live || !on[j]) continue;
-            if (a.quant) {
-                if (e % a.quant == 0) a.scales[row * (dim / a.quant) + e / a.quant] = scale;
-                const float inv = 1.f / scale;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) h[j][i] *= inv;
-                store_e4m3<VEC>(a.y8 + row * dim + e, h[j]);
+                    for (int i = 0; i < VEC; ++i) m = max_nan(m, fabsf(h[j][i]));
+                    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                    if (VEC == 4 || a.quant > 32)
+                        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                    if (a.quant > (VEC == 4 ? 32 : 64))
+                        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                    if (VEC == 4 && a.quant > 64)
+                        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                    scale = max_nan(m * (1.f / kE4m3Max), kMinScale);
+                }
+                if (!live || !w.on[j]) continue;
+                if constexpr (kQuant == kPerRow) {
+                    if (e == 0) a.scales[w.row] = scale;
+                } else if ((e & (a.quant - 1)) == 0) {
+                    const int shift = 31 - __clz(a.quant);
+                    a.scales[w.row * (dim >> shift) + (e >> shift)] = scale;
+                }
+                float inv;   // of a scale between 1e-30 and 1e36: to 2^-23
+                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+                times(h[j], inv);
+                store_e4m3<VEC>(a.y8 + w.row * dim + e, h[j]);
             } else {
-                store<T, VEC>(a.y, row * dim + e, h[j]);
+                if (!live || !w.on[j]) continue;
+                store<T, VEC>(a.y, w.at(j), h[j]);
             }
         }
+        w.next();
     }
 }
 
-template <typename T, int VEC, int NV, int TPR>
+// The same walk.  The operands stay in registers as loaded (bf16 in half of them) and are taken
+// apart again behind the reduction; the gate's sigmoid is formed again, too.
+template <typename T, int VEC, int NV, int TPR, int kMode>
 __global__ void __launch_bounds__(TPR == 0 ? kMaxRowThreads : kRowThreads)
 rms_norm_bwd_kernel(const NormArgs a)
 {
     __shared__ float2 red[2 * (kMaxRowThreads / 32)];
-    const int tpr = threads_per_row<TPR>();
-    const int rows_per_cta = TPR == 0 ? 1 : kRowThreads / tpr;
-    const int lane = TPR == 0 ? threadIdx.x : threadIdx.x % tpr;
+    extern __shared__ __align__(16) char ring[];
+    constexpr bool kGated = kMode == kPre || kMode == kPost;
     const int dim = a.dim;
     const float inv_dim = 1.f / (float)dim;
-    float w[NV][VEC], dw[NV][VEC];
-    bool on[NV];
+    Walk<T, VEC, NV, TPR, norm_bwd_ops(kMode)> w(a, ring);
+    w.op[0] = a.x;
+    w.op[1] = a.dy;
+    if constexpr (kMode != kPlain) w.op[2] = kGated ? a.z : a.dres;
+    w.start();
+    float wt[NV][VEC], dw[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int e = (j * tpr + lane) * VEC;
-        on[j] = e < dim;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) w[j][i] = dw[j][i] = 0.f;
-        if (on[j]) load_w<VEC>(a.w + e, w[j]);
+        for (int i = 0; i < VEC; ++i) wt[j][i] = dw[j][i] = 0.f;
+        if (w.on[j]) load_w<VEC>(a.w + (j * w.tpr + w.lane) * VEC, wt[j]);
     }
-    int buf = 0;
-    const int64_t step = (int64_t)gridDim.x * rows_per_cta;
-    const int64_t first = (int64_t)blockIdx.x * rows_per_cta;
-    const int sub = TPR == 0 ? 0 : threadIdx.x / tpr;
-    for (int64_t base = first; base < a.rows; base += step, buf ^= 1) {
-        const int64_t row = base + sub;
-        const bool live = row < a.rows;
-        // x and z stay as loaded; dn w h and h h are reduced, then dn and h are formed again
-        float x[NV][VEC], z[NV][VEC], dy[NV][VEC];
-        float ss = 0.f, dot = 0.f;
+    for (int buf = 0; w.more(); buf ^= 1) {
+        const bool live = w.live();
+        Pack<T, VEC> xp[NV], yp[NV], tp[NV];
+        uint64_t sums = 0, dots = 0;
+        w.arrived();
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t at = row * dim + (j * tpr + lane) * VEC;
+            if (!live || !w.on[j]) continue;
+            xp[j] = w.get(0, j);
+            yp[j] = w.get(1, j);
+            if constexpr (kMode != kPlain) tp[j] = w.get(2, j);
+            float x[VEC], dy[VEC], z[VEC];
+            xp[j].get(x);
+            yp[j].get(dy);
+            if constexpr (kGated) tp[j].get(z);
+            if constexpr (kGated) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) x[j][i] = dy[j][i] = z[j][i] = 0.f;
-            if (live && on[j]) {
-                load<T, VEC>(a.x, at, x[j]);
-                load<T, VEC>(a.dy, at, dy[j]);
-                if (a.gate) load<T, VEC>(a.z, at, z[j]);
+                for (int i = 0; i < VEC; ++i) z[i] *= sigmoid(z[i]);
+                if constexpr (kMode == kPre) times(x, z);
+                else times(dy, z);
             }
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                float h = x[j][i], dn = dy[j][i];
-                if (a.gate) {
-                    const float s = z[j][i] * sigmoid(z[j][i]);
-                    if (a.gate == 1) h *= s;
-                    else dn *= s;
-                }
-                ss = fmaf(h, h, ss);
-                dot = fmaf(dn * w[j][i], h, dot);
-            }
+            add_products(sums, x, x);
+            times(dy, wt[j]);
+            add_products(dots, dy, x);
         }
+        float ss = both(sums), dot = both(dots);
         reduce_row<TPR, false>(ss, dot, red, buf);
         const float r = rsqrtf(fmaf(ss, inv_dim, a.eps));
         const float c = dot * inv_dim * r * r * r;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            if (!live || !on[j]) continue;
-            const int64_t at = row * dim + (j * tpr + lane) * VEC;
-            float dx[VEC], dz[VEC];
-            float dres[VEC];
-            if (a.dres) load<T, VEC>(a.dres, at, dres);
+            if (!live || !w.on[j]) continue;
+            float x[VEC], dy[VEC], t[VEC], dx[VEC], dz[VEC];
+            xp[j].get(x);
+            yp[j].get(dy);
+            if constexpr (kMode != kPlain) tp[j].get(t);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                float h = x[j][i], dn = dy[j][i], s = 0.f, slope = 0.f;
-                if (a.gate) {   // silu and its derivative
-                    const float g = sigmoid(z[j][i]);
-                    s = z[j][i] * g;
-                    slope = g * fmaf(z[j][i], 1.f - g, 1.f);
-                    if (a.gate == 1) h *= s;
+                float h = x[i], dn = dy[i], s = 0.f, slope = 0.f;
+                if constexpr (kGated) {   // silu and its derivative
+                    const float g = sigmoid(t[i]);
+                    s = t[i] * g;
+                    slope = g * fmaf(t[i], 1.f - g, 1.f);
+                    if constexpr (kMode == kPre) h *= s;
                     else dn *= s;
                 }
                 const float n = h * r;
-                const float dh = fmaf(r * dn, w[j][i], -h * c);
+                const float dh = fmaf(r * dn, wt[j][i], -h * c);
                 dw[j][i] = fmaf(dn, n, dw[j][i]);
-                dx[i] = a.gate == 1 ? dh * s : a.dres ? dh + dres[i] : dh;
-                dz[i] = (a.gate == 1 ? dh * x[j][i] : dy[j][i] * n * w[j][i]) * slope;
+                dx[i] = kMode == kPre ? dh * s : kMode == kResidual ? dh + t[i] : dh;
+                if constexpr (kGated)
+                    dz[i] = (kMode == kPre ? dh * x[i] : dy[i] * n * wt[j][i]) * slope;
             }
-            store<T, VEC>(a.dx, at, dx);
-            if (a.gate) store<T, VEC>(a.dz, at, dz);
+            store<T, VEC>(a.dx, w.at(j), dx);
+            if constexpr (kGated) store<T, VEC>(a.dz, w.at(j), dz);
         }
+        w.next();
     }
     // this CTA's partial weight gradient: one row of `dw_part`
     if constexpr (TPR == 0) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (on[j])
+            if (w.on[j])
 #pragma unroll
                 for (int i = 0; i < VEC; ++i)
-                    a.dw_part[(int64_t)blockIdx.x * dim + (j * tpr + lane) * VEC + i] = dw[j][i];
-    } else {   // the CTA's rows are added up in order
-        extern __shared__ float part[];   // rows_per_cta x dim
+                    a.dw_part[(int64_t)blockIdx.x * dim + (j * w.tpr + w.lane) * VEC + i] = dw[j][i];
+    } else {   // the CTA's rows are added up in order, in the ring's place
+        constexpr int kPer = kRowThreads / (TPR == 0 ? kRowThreads : TPR);
+        float *part = reinterpret_cast<float *>(ring);   // kPer x dim
+        cp_wait<0>();
+        __syncthreads();
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (on[j])
+            if (w.on[j])
 #pragma unroll
                 for (int i = 0; i < VEC; ++i)
-                    part[sub * dim + (j * tpr + lane) * VEC + i] = dw[j][i];
+                    part[w.sub * dim + (j * w.tpr + w.lane) * VEC + i] = dw[j][i];
         __syncthreads();
         for (int e = threadIdx.x; e < dim; e += kRowThreads) {
             float s = 0.f;
-            for (int k = 0; k < rows_per_cta; ++k) s += part[k * dim + e];
+            for (int k = 0; k < kPer; ++k) s += part[k * dim + e];
             a.dw_part[(int64_t)blockIdx.x * dim + e] = s;
         }
     }
 }
 
-// dw[e] = the sum of n rows of partial sums: 32 columns per CTA, the rows dealt to 8 warps, the
-// warps' sums added in order, so repeated calls give the same bits.
-__global__ void __launch_bounds__(256)
+// dw[e] = the sum of n rows of partial sums: 32 columns per CTA, the rows dealt to 32 warps, the
+// warps' sums added in order, so repeated calls give the same bits.  (Dealt to 8 warps it took
+// 25 us for 592 rows of 2560: the loads' latency, 19 times over.)
+__global__ void __launch_bounds__(1024)
 rms_norm_dw_kernel(const float *part, float *dw, int n, int dim)
 {
-    __shared__ float sums[8][32];
-    const int col = blockIdx.x * 32 + threadIdx.x % 32, warp = threadIdx.x / 32;
-    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+    __shared__ float sums[32][33];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, col = blockIdx.x * 32 + lane;
+    float s[4] = {};
     if (col < dim) {
-        int r = warp;
-        for (; r + 24 < n; r += 32) {
-            s0 += part[(int64_t)r * dim + col];
-            s1 += part[(int64_t)(r + 8) * dim + col];
-            s2 += part[(int64_t)(r + 16) * dim + col];
-            s3 += part[(int64_t)(r + 24) * dim + col];
+        const float *p = part + col;
+#pragma unroll
+        for (int k = 0; k < kBwdCtas / 32; k += 4) {   // all loads at once
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = warp + (k + i) * 32;
+                s[i] += k + i < kBwdCtas / 32 && r < n ? p[(int64_t)r * dim] : 0.f;
+            }
         }
-        for (; r < n; r += 8) s0 += part[(int64_t)r * dim + col];
     }
-    sums[warp][threadIdx.x % 32] = (s0 + s1) + (s2 + s3);
+    sums[warp][lane] = (s[0] + s[1]) + (s[2] + s[3]);
     __syncthreads();
-    if (warp == 0 && col < dim) {
-        float s = 0.f;
-        for (int i = 0; i < 8; ++i) s += sums[i][threadIdx.x];
-        dw[col] = s;
-    }
+    float t = sums[lane][warp];   // column `warp`, a lane per row warp
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lane == 0 && blockIdx.x * 32 + warp < dim) dw[blockIdx.x * 32 + warp] = t;
 }
 
 int sm_count()
@@ -407,64 +563,100 @@ int sm_count()
     return n;
 }
 
-int64_t bwd_ctas(int64_t rows, int rows_per_cta)
+// Launches a walk of `rows` rows, per_cta at a time, on as many CTAs as the GPU holds at once.
+template <typename K>
+cudaError_t launch_walk(K kern, const NormArgs &a, int per_cta, int threads, size_t smem, int64_t most,
+                        int64_t *ctas, cudaStream_t st)
 {
-    const int64_t need = (rows + rows_per_cta - 1) / rows_per_cta;
-    return need < kBwdCtas ? need : kBwdCtas;
+    cudaError_t e;
+    if (smem > 40 * 1024) {   // with the static part this may pass 48 KB
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    int64_t grid = (a.rows + per_cta - 1) / per_cta;
+    const int64_t sms = sm_count();
+    if (grid > sms) {
+        int per_sm = 1;
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
+        if (e != cudaSuccess) return e;
+        if (grid > sms * per_sm) grid = sms * (per_sm > 0 ? per_sm : 1);
+    }
+    if (grid > most) grid = most;
+    if (ctas) *ctas = grid;
+    kern<<<(unsigned)grid, threads, smem, st>>>(a);
+    return cudaGetLastError();
 }
 
-template <typename T, int VEC, int NV, int TPR>
+template <typename T, int VEC, int NV, int TPR, int kMode>
 cudaError_t launch(const NormArgs &a, bool bwd, int threads, float *dw, cudaStream_t st)
 {
     const int per_cta = TPR == 0 ? 1 : kRowThreads / TPR;
-    const int64_t need = (a.rows + per_cta - 1) / per_cta;
+    const size_t slots = sizeof(T) * VEC == 16 ? (size_t)rows_ahead(NV) * NV * threads * 16 : 0;
     if (!bwd) {
-        // enough CTAs to fill every SM's threads; each walks the rows with w in registers
-        const int64_t most = (int64_t)sm_count() * (2048 / threads);
-        rms_norm_kernel<T, VEC, NV, TPR>
-            <<<(unsigned)(need < most ? need : most), threads, 0, st>>>(a);
-        return cudaGetLastError();
+        const size_t smem = slots * norm_ops(kMode);
+        auto go = [&](auto kern) {
+            return launch_walk(kern, a, per_cta, threads, smem, 1 << 30, nullptr, st);
+        };
+        if (!a.quant) return go(rms_norm_kernel<T, VEC, NV, TPR, kMode, kNoQuant>);
+        if (a.quant == a.dim) return go(rms_norm_kernel<T, VEC, NV, TPR, kMode, kPerRow>);
+        if constexpr (VEC > 1)   // a group of 32 or more divides dim: whole vectors
+            return go(rms_norm_kernel<T, VEC, NV, TPR, kMode, kPerGroup>);
+        return cudaErrorInvalidValue;
     }
-    const int64_t ctas = bwd_ctas(a.rows, per_cta);
-    const size_t smem = TPR == 0 ? 0 : (size_t)per_cta * a.dim * sizeof(float);
-    rms_norm_bwd_kernel<T, VEC, NV, TPR><<<(unsigned)ctas, threads, smem, st>>>(a);
-    cudaError_t e = cudaGetLastError();
+    size_t smem = slots * norm_bwd_ops(kMode);
+    const size_t part = TPR == 0 ? 0 : (size_t)per_cta * a.dim * sizeof(float);
+    smem = std::max(smem, part);
+    int64_t ctas = 0;
+    cudaError_t e = launch_walk(rms_norm_bwd_kernel<T, VEC, NV, TPR, kMode>, a, per_cta, threads,
+                                smem, kBwdCtas, &ctas, st);
     if (e != cudaSuccess) return e;
-    rms_norm_dw_kernel<<<(a.dim + 31) / 32, 256, 0, st>>>(a.dw_part, dw, (int)ctas, a.dim);
+    rms_norm_dw_kernel<<<(a.dim + 31) / 32, 1024, 0, st>>>(a.dw_part, dw, (int)ctas, a.dim);
     return cudaGetLastError();
 }
 
 // Threads of a CTA that takes one row of `vecs` vectors, NV per thread.
 int row_threads(int vecs, int nv) { return ((vecs + nv - 1) / nv + 31) / 32 * 32; }
 
-// Rows of up to 32 vectors on 8, 16 or 32 lanes (no barrier), up to 128 vectors on a warp with
-// four each, longer ones on a CTA with as few vectors per thread as its 512 threads allow.
-template <typename T, int VEC>
+// Rows of up to 32 vectors on 8, 16 or 32 lanes (no barrier), longer ones on a CTA with as few
+// vectors per thread as its 512 threads allow.
+template <typename T, int VEC, int kMode>
 cudaError_t launch_sized(const NormArgs &a, bool bwd, float *dw, cudaStream_t st)
 {
     const int vecs = (a.dim + VEC - 1) / VEC;
-    constexpr int kMost = 32 / VEC;   // vectors per thread that hold 32 elements
-    if (vecs <= 8) return launch<T, VEC, 1, 8>(a, bwd, kRowThreads, dw, st);
-    if (vecs <= 16) return launch<T, VEC, 1, 16>(a, bwd, kRowThreads, dw, st);
-    if (vecs <= 32) return launch<T, VEC, 1, 32>(a, bwd, kRowThreads, dw, st);
-    if (vecs <= 128) return launch<T, VEC, 4, 32>(a, bwd, kRowThreads, dw, st);
-    if (vecs <= kMaxRowThreads) return launch<T, VEC, 1, 0>(a, bwd, row_threads(vecs, 1), dw, st);
+    if (vecs <= 8) return launch<T, VEC, 1, 8, kMode>(a, bwd, kRowThreads, dw, st);
+    if (vecs <= 16) return launch<T, VEC, 1, 16, kMode>(a, bwd, kRowThreads, dw, st);
+    if (vecs <= 32) return launch<T, VEC, 1, 32, kMode>(a, bwd, kRowThreads, dw, st);
+    if (vecs <= kMaxRowThreads)
+        return launch<T, VEC, 1, 0, kMode>(a, bwd, row_threads(vecs, 1), dw, st);
     if (vecs <= 2 * kMaxRowThreads)
-        return launch<T, VEC, 2, 0>(a, bwd, row_threads(vecs, 2), dw, st);
+        return launch<T, VEC, 2, 0, kMode>(a, bwd, row_threads(vecs, 2), dw, st);
     if (vecs <= 4 * kMaxRowThreads)
-        return launch<T, VEC, 4, 0>(a, bwd, row_threads(vecs, 4), dw, st);
-    if constexpr (kMost > 4)
-        return launch<T, VEC, kMost, 0>(a, bwd, row_threads(vecs, kMost), dw, st);
+        return launch<T, VEC, 4, 0, kMode>(a, bwd, row_threads(vecs, 4), dw, st);
+    if constexpr (VEC <= 4) {
+        if (vecs <= 8 * kMaxRowThreads)
+            return launch<T, VEC, 8, 0, kMode>(a, bwd, row_threads(vecs, 8), dw, st);
+    }
+    if constexpr (VEC == 1)
+        return launch<T, VEC, 32, 0, kMode>(a, bwd, row_threads(vecs, 32), dw, st);
     return cudaErrorInvalidValue;   // not reached: kMaxDim elements fit
+}
+
+template <typename T, int VEC>
+cudaError_t launch_mode(const NormArgs &a, bool bwd, float *dw, cudaStream_t st)
+{
+    if (a.gate == SSD_GATE_PRE) return launch_sized<T, VEC, kPre>(a, bwd, dw, st);
+    if (a.gate == SSD_GATE_POST) return launch_sized<T, VEC, kPost>(a, bwd, dw, st);
+    if (bwd ? a.dres : a.residual) return launch_sized<T, VEC, kResidual>(a, bwd, dw, st);
+    return launch_sized<T, VEC, kPlain>(a, bwd, dw, st);
 }
 
 cudaError_t launch_norm(const NormArgs &a, bool is_bf16, bool bwd, float *dw, cudaStream_t st)
 {
     if (is_bf16)
-        return a.dim % 8 ? launch_sized<bf16, 1>(a, bwd, dw, st)
-                         : launch_sized<bf16, 8>(a, bwd, dw, st);
-    return a.dim % 4 ? launch_sized<float, 1>(a, bwd, dw, st)
-                     : launch_sized<float, 4>(a, bwd, dw, st);
+        return a.dim % 8 ? launch_mode<bf16, 1>(a, bwd, dw, st)
+                         : launch_mode<bf16, 8>(a, bwd, dw, st);
+    return a.dim % 4 ? launch_mode<float, 1>(a, bwd, dw, st)
+                     : launch_mode<float, 4>(a, bwd, dw, st);
 }
 
 ssd_status check_norm(const ssd_norm_desc *d)
