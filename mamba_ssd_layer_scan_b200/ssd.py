@@ -22,6 +22,7 @@ stands in front of and behind either mixer:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import Optional
@@ -186,9 +187,15 @@ def workspace_size(shape: Shape, chunk_size: int) -> int:
 
 
 # ---------------------------------------------------------------- torch marshalling
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
@@ -538,70 +545,116 @@ def state_update(state, x, dt, A, B, C, D, y=None, stream=None, z=None, dt_bias=
 
 
 # ---------------------------------------------------------------- gated delta rule
+# One token's step takes a few microseconds on the GPU: these calls look at each tensor once, and
+# keep what depends on a call's sizes alone (its description, its workspace's size).
 def _on(t, name, shape, dtype, device):
-    """Refuse what the kernels would misread: another shape, type, device, or strides."""
-    _require(t, name, dtype, device)
-    if tuple(t.shape) != tuple(shape):
+    """Refuse what the kernels would misread: another shape, type, device (its index), or strides."""
+    if (t.shape != shape or t.dtype is not dtype or t.get_device() != device
+            or not t.is_contiguous()):
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != device:
+            where = "a CUDA device" if device < 0 else f"cuda:{device}"
+            raise ValueError(f"{name} must be on {where}, got {t.device}")
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 class _Call:
     """A call's device and stream (the device's current stream by default): allocates outputs and
     workspaces, and keeps their memory from being handed out again while that stream uses it."""
+    __slots__ = ("torch", "device", "handle", "other")
 
     def __init__(self, x, stream):
-        torch = _torch()
+        self.torch = torch = _torch()
         if not x.is_cuda:
             raise ValueError(f"tensors must be on a CUDA device, got {x.device}")
-        self.device = x.device
-        self.own = torch.cuda.current_stream(x.device)
-        self.stream = self.own if stream is None else stream
-        if self.stream.device != x.device:
-            raise ValueError(f"the stream is on {self.stream.device}, the tensors on {x.device}")
+        self.device = x.get_device()
+        self.handle = torch._C._cuda_getCurrentRawStream(self.device)
+        self.other = None
+        if stream is not None:
+            if stream.device != x.device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {x.device}")
+            if stream.cuda_stream != self.handle:
+                self.handle, self.other = stream.cuda_stream, stream
 
     def empty(self, shape, dtype):
-        torch = _torch()
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.stream != self.own:
-            t.record_stream(self.stream)
+        t = self.torch.empty(shape, dtype=dtype, device=self.device)
+        if self.other is not None:
+            t.record_stream(self.other)
         return t
 
     def workspace(self, given, size):
-        torch = _torch()
         if given is None:
-            return self.empty(size, torch.uint8)
-        _require(given, "workspace", torch.uint8, self.device)
+            return self.empty(size, self.torch.uint8)
+        _on(given, "workspace", given.shape, self.torch.uint8, self.device)
         return given
 
     def run(self, function, *args):
-        torch = _torch()
-        with torch.cuda.device(self.device):
-            _check(function(*args, self.stream.cuda_stream))
+        cuda = self.torch.cuda
+        if cuda.current_device() == self.device:
+            status = function(*args, self.handle)
+        else:
+            with cuda.device(self.device):
+                status = function(*args, self.handle)
+        _check(status)
+
+
+class _DeltaPlan:
+    """What the calls of one shape have in common."""
+
+    def __init__(self, *shape):
+        self.shape = make_shape(*shape)
+        self.ref = ctypes.byref(self.shape)
+        self.sizes = {}
+
+    def workspace_size(self, query, *args):
+        n = self.sizes.get((query, *args))
+        if n is None:
+            n = getattr(lib(), query)(self.ref, *args)
+            if n == 0:
+                raise SSDError(SSD_ERR_INVALID_ARG, last_error())
+            self.sizes[(query, *args)] = n
+        return n
+
+
+_delta_plan = functools.lru_cache(maxsize=512)(_DeltaPlan)
 
 
 def _delta_inputs(q, k, v, g, beta, state_rows, states, seq=True):
-    """Shape of the call after every tensor has been checked against q, k and v."""
-    torch = _torch()
+    """The call's plan after every tensor has been checked against q, k and v."""
     if v.dim() != (4 if seq else 3) or q.dim() != v.dim():
         raise ValueError("q, k and v must be (batch, seqlen, heads, width)" if seq else
                          "q, k and v must be (batch, heads, width)")
-    lead, (H, P), (G, N) = tuple(v.shape[:-2]), v.shape[-2:], q.shape[-2:]
-    code = _dtype_code(v)
-    _on(v, "v", v.shape, v.dtype, v.device)
-    for t, n in ((q, "q"), (k, "k")):
-        _on(t, n, lead + (G, N), v.dtype, v.device)
+    code, dtype, f32 = _dtype_code(v), v.dtype, _torch().float32
+    # tensors elsewhere than v, or on the CPU, are refused by name; v on the CPU by the call
+    device = v.get_device()
+    if not v.is_contiguous():
+        raise ValueError("v must be contiguous")
+    if seq:
+        b, L, H, P = v.shape
+        G, N = q.shape[2:]
+        rows, per_head = (b, L, G, N), (b, L, H)
+    else:
+        (b, H, P), L = v.shape, 1
+        G, N = q.shape[1:]
+        rows, per_head = (b, G, N), (b, H)
+    _on(q, "q", rows, dtype, device)
+    _on(k, "k", rows, dtype, device)
     if g is not None:
-        _on(g, "g", lead + (H,), torch.float32, v.device)
-    _on(beta, "beta", lead + (H,), torch.float32, v.device)
-    rows = lead[0] if state_rows is None else state_rows
+        _on(g, "g", per_head, f32, device)
+    _on(beta, "beta", per_head, f32, device)
     for t, n in states:
         if t is not None:
-            _on(t, n, (rows, H, P, N), torch.float32, v.device)
-    return make_shape(lead[0], lead[1] if seq else 1, H, P, N, G, code)
+            _on(t, n, (b if state_rows is None else state_rows, H, P, N), f32, device)
+    return _delta_plan(b, L, H, P, N, G, code)
 
 
-def _delta_options(scale, dstate, qk_l2norm) -> DeltaOptions:
-    return DeltaOptions(dstate ** -0.5 if scale is None else scale, 1 if qk_l2norm else 0)
+@functools.lru_cache(maxsize=64)
+def _delta_options(scale, dstate, qk_l2norm):
+    return ctypes.byref(DeltaOptions(dstate ** -0.5 if scale is None else scale,
+                                     1 if qk_l2norm else 0))
 
 
 def delta_rule_workspace_size(shape: Shape) -> int:
@@ -618,20 +671,20 @@ def delta_rule_fwd(q, k, v, g, beta, scale=None, init_state=None, qk_l2norm: boo
     (b, L, H, P) float32 or bf16, g (b, L, H) float32 log-decay or None, beta (b, L, H) float32,
     init_state (b, H, P, N) float32 or None; scale defaults to N ** -0.5.  Returns
     (o, final_state or None)."""
-    torch = _torch()
-    shape = _delta_inputs(q, k, v, g, beta, None,
-                          ((init_state, "init_state"), (final_state, "final_state")))
-    call = _Call(v, stream)
+    plan = _delta_inputs(q, k, v, g, beta, None,
+                         ((init_state, "init_state"), (final_state, "final_state")))
+    call, shape = _Call(v, stream), plan.shape
     if o is None:
         o = call.empty(v.shape, v.dtype)
-    _on(o, "o", v.shape, v.dtype, v.device)
+    else:
+        _on(o, "o", v.shape, v.dtype, call.device)
     if final_state is None and return_final_state:
         final_state = call.empty((shape.batch, shape.nheads, shape.headdim, shape.dstate),
-                                 torch.float32)
-    workspace = call.workspace(workspace, delta_rule_workspace_size(shape))
-    call.run(lib().ssd_delta_rule_fwd, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
-             _ptr(beta), ctypes.byref(_delta_options(scale, shape.dstate, qk_l2norm)),
-             _ptr(init_state), _ptr(o), _ptr(final_state), _ptr(workspace), workspace.numel())
+                                 call.torch.float32)
+    workspace = call.workspace(workspace, plan.workspace_size("ssd_delta_rule_workspace_size"))
+    call.run(lib().ssd_delta_rule_fwd, plan.ref, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+             _delta_options(scale, shape.dstate, qk_l2norm), _ptr(init_state), _ptr(o),
+             _ptr(final_state), _ptr(workspace), workspace.numel())
     return o, final_state
 
 
@@ -641,25 +694,22 @@ def delta_rule_varlen_fwd(q, k, v, g, beta, cu_seqlens, scale=None, init_states=
     """The gated delta rule over packed sequences (ssd_delta_rule_varlen_fwd): tensors as for
     delta_rule_fwd with batch 1, cu_seqlens (nseq + 1,) int32 on the device, states (nseq, H, P, N).
     Returns (o, final_states or None)."""
-    torch = _torch()
     nseq = cu_seqlens.numel() - 1
-    shape = _delta_inputs(q, k, v, g, beta, nseq,
-                          ((init_states, "init_states"), (final_states, "final_states")))
-    _on(cu_seqlens, "cu_seqlens", (nseq + 1,), torch.int32, v.device)
-    call = _Call(v, stream)
+    plan = _delta_inputs(q, k, v, g, beta, nseq,
+                         ((init_states, "init_states"), (final_states, "final_states")))
+    _on(cu_seqlens, "cu_seqlens", (nseq + 1,), _torch().int32, v.get_device())
+    call, shape = _Call(v, stream), plan.shape
     if o is None:
         o = call.empty(v.shape, v.dtype)
-    _on(o, "o", v.shape, v.dtype, v.device)
-    n = lib().ssd_delta_rule_varlen_workspace_size(ctypes.byref(shape), nseq)
-    if n == 0:
-        raise SSDError(SSD_ERR_INVALID_ARG, last_error())
+    else:
+        _on(o, "o", v.shape, v.dtype, call.device)
+    n = plan.workspace_size("ssd_delta_rule_varlen_workspace_size", nseq)
     if final_states is None and return_final_states:
         final_states = call.empty((nseq, shape.nheads, shape.headdim, shape.dstate),
-                                  torch.float32)
+                                  call.torch.float32)
     workspace = call.workspace(workspace, n)
-    call.run(lib().ssd_delta_rule_varlen_fwd, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v),
-             _ptr(g), _ptr(beta),
-             ctypes.byref(_delta_options(scale, shape.dstate, qk_l2norm)), _ptr(cu_seqlens), nseq,
+    call.run(lib().ssd_delta_rule_varlen_fwd, plan.ref, _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+             _ptr(beta), _delta_options(scale, shape.dstate, qk_l2norm), _ptr(cu_seqlens), nseq,
              _ptr(init_states), _ptr(o), _ptr(final_states), _ptr(workspace), workspace.numel())
     return o, final_states
 
@@ -670,26 +720,23 @@ def delta_rule_bwd(q, k, v, g, beta, dout, scale=None, init_state=None, dfinal=N
     """Gradients of delta_rule_fwd (ssd_delta_rule_bwd), given dout (like o) and dfinal
     (b, H, P, N) float32 or None: a dict of dq, dk, dv (bf16, like q, k, v), dg (None without g)
     and dbeta (b, L, H) float32, dinit (b, H, P, N) float32 (None unless return_dinit)."""
-    torch = _torch()
-    shape = _delta_inputs(q, k, v, g, beta, None, ((init_state, "init_state"),
-                                                   (dfinal, "dfinal")))
-    _on(dout, "dout", v.shape, v.dtype, v.device)
-    call = _Call(v, stream)
-    n = lib().ssd_delta_rule_bwd_workspace_size(ctypes.byref(shape))
-    if n == 0:
-        raise SSDError(SSD_ERR_UNSUPPORTED, last_error())
-    out = {"d" + name: call.empty(t.shape, t.dtype)
-           for name, t in (("q", q), ("k", k), ("v", v))}
-    out["dg"] = None if g is None else call.empty(g.shape, torch.float32)
-    out["dbeta"] = call.empty(beta.shape, torch.float32)
-    out["dinit"] = call.empty((shape.batch, shape.nheads, shape.headdim, shape.dstate),
-                              torch.float32) if return_dinit else None
+    plan = _delta_inputs(q, k, v, g, beta, None, ((init_state, "init_state"),
+                                                  (dfinal, "dfinal")))
+    _on(dout, "dout", v.shape, v.dtype, v.get_device())
+    call, shape = _Call(v, stream), plan.shape
+    n = plan.workspace_size("ssd_delta_rule_bwd_workspace_size")
+    f32 = call.torch.float32
+    out = dict(dq=call.empty(q.shape, q.dtype), dk=call.empty(k.shape, k.dtype),
+               dv=call.empty(v.shape, v.dtype),
+               dg=None if g is None else call.empty(g.shape, f32),
+               dbeta=call.empty(beta.shape, f32),
+               dinit=call.empty((shape.batch, shape.nheads, shape.headdim, shape.dstate), f32)
+               if return_dinit else None)
     workspace = call.workspace(workspace, n)
-    call.run(lib().ssd_delta_rule_bwd, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
-             _ptr(beta), ctypes.byref(_delta_options(scale, shape.dstate, qk_l2norm)),
-             _ptr(init_state), _ptr(dout), _ptr(dfinal), _ptr(out["dq"]), _ptr(out["dk"]),
-             _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dbeta"]), _ptr(out["dinit"]),
-             _ptr(workspace), workspace.numel())
+    call.run(lib().ssd_delta_rule_bwd, plan.ref, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+             _delta_options(scale, shape.dstate, qk_l2norm), _ptr(init_state), _ptr(dout),
+             _ptr(dfinal), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]),
+             _ptr(out["dbeta"]), _ptr(out["dinit"]), _ptr(workspace), workspace.numel())
     return out
 
 
@@ -698,36 +745,50 @@ def delta_rule_update(state, q, k, v, g, beta, scale=None, qk_l2norm: bool = Fal
     """One token per sequence (ssd_delta_rule_update).  state (b, H, P, N) float32 (in place),
     q, k (b, G, N), v (b, H, P), g (b, H) float32 or None, beta (b, H) float32.  Returns
     o (b, H, P)."""
-    shape = _delta_inputs(q, k, v, g, beta, None, ((state, "state"),), seq=False)
+    plan = _delta_inputs(q, k, v, g, beta, None, ((state, "state"),), seq=False)
     call = _Call(v, stream)
     if o is None:
         o = call.empty(v.shape, v.dtype)
-    _on(o, "o", v.shape, v.dtype, v.device)
-    call.run(lib().ssd_delta_rule_update, ctypes.byref(shape), _ptr(state), _ptr(q), _ptr(k),
-             _ptr(v), _ptr(g), _ptr(beta),
-             ctypes.byref(_delta_options(scale, shape.dstate, qk_l2norm)), _ptr(o))
+    else:
+        _on(o, "o", v.shape, v.dtype, call.device)
+    call.run(lib().ssd_delta_rule_update, plan.ref, _ptr(state), _ptr(q), _ptr(k), _ptr(v),
+             _ptr(g), _ptr(beta), _delta_options(scale, plan.shape.dstate, qk_l2norm), _ptr(o))
     return o
 
 
 # ---------------------------------------------------------------- RMS norm
-def _norm_desc(x, weight, eps, z, gate, quant_group, others) -> NormDesc:
-    """The call's description after every tensor has been checked against x."""
-    torch = _torch()
+class _NormPlan:
+    def __init__(self, *desc):
+        self.desc = NormDesc(*desc)
+        self.ref = ctypes.byref(self.desc)
+        self.bwd_size = lib().ssd_rms_norm_bwd_workspace_size(self.ref)
+
+
+_norm_plan = functools.lru_cache(maxsize=512)(_NormPlan)
+
+
+def _norm_inputs(x, weight, eps, z, gate, quant_group, others) -> _NormPlan:
+    """The call's plan after every tensor has been checked against x."""
     if gate not in GATES:
         raise ValueError(f"gate must be one of {sorted(GATES)}, got {gate!r}")
     if (gate != "none") != (z is not None):
         raise ValueError("z goes with a gate, and a gate with z")
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError(f"x must be (..., dim), got {tuple(x.shape)}")
-    dim = x.shape[-1]
+    shape, dtype, device = x.shape, x.dtype, x.get_device()
+    dim = shape[-1]
     if quant_group and (quant_group < 0 or dim % quant_group):
         raise ValueError(f"quant_group must divide dim {dim}, got {quant_group}")
     code = _dtype_code(x)
-    for t, n in ((x, "x"), (z, "z")) + others:
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    if z is not None:
+        _on(z, "z", shape, dtype, device)
+    for t, n in others:
         if t is not None:
-            _on(t, n, x.shape, x.dtype, x.device)
-    _on(weight, "weight", (dim,), torch.float32, x.device)
-    return NormDesc(x.numel() // dim, dim, code, GATES[gate], quant_group, eps)
+            _on(t, n, shape, dtype, device)
+    _on(weight, "weight", (dim,), _torch().float32, device)
+    return _norm_plan(x.numel() // dim, dim, code, GATES[gate], quant_group, eps)
 
 
 def rms_norm(x, weight, eps: float = 1e-5, residual=None, z=None, gate: str = "none",
@@ -738,27 +799,29 @@ def rms_norm(x, weight, eps: float = 1e-5, residual=None, z=None, gate: str = "n
     quant_group: y in float8_e4m3fn with one float32 scale per quant_group elements (dim: per
     row).  Returns y, followed by the scales (..., dim // quant_group) if quantised and by
     residual_out if there is a residual; y alone where neither is."""
-    torch = _torch()
-    desc = _norm_desc(x, weight, eps, z, gate, quant_group,
-                      ((residual, "residual"), (residual_out, "residual_out")))
+    plan = _norm_inputs(x, weight, eps, z, gate, quant_group,
+                        ((residual, "residual"), (residual_out, "residual_out")))
     if residual is None and residual_out is not None:
         raise ValueError("residual_out goes with residual")
     call = _Call(x, stream)
+    torch = call.torch
     out_dtype = torch.float8_e4m3fn if quant_group else x.dtype
     if y is None:
         y = call.empty(x.shape, out_dtype)
-    _on(y, "y", x.shape, out_dtype, x.device)
+    else:
+        _on(y, "y", x.shape, out_dtype, call.device)
     if quant_group:
-        shape = tuple(x.shape[:-1]) + (x.shape[-1] // quant_group,)
+        shape = x.shape[:-1] + (x.shape[-1] // quant_group,)
         if scales is None:
             scales = call.empty(shape, torch.float32)
-        _on(scales, "scales", shape, torch.float32, x.device)
+        else:
+            _on(scales, "scales", shape, torch.float32, call.device)
     elif scales is not None:
         raise ValueError("scales go with quant_group")
     if residual is not None and residual_out is None:
         residual_out = call.empty(x.shape, x.dtype)
-    call.run(lib().ssd_rms_norm, ctypes.byref(desc), _ptr(x), _ptr(residual), _ptr(z),
-             _ptr(weight), _ptr(y), _ptr(scales), _ptr(residual_out))
+    call.run(lib().ssd_rms_norm, plan.ref, _ptr(x), _ptr(residual), _ptr(z), _ptr(weight), _ptr(y),
+             _ptr(scales), _ptr(residual_out))
     out = [t for t in (y, scales, residual_out) if t is not None]
     return out[0] if len(out) == 1 else tuple(out)
 
@@ -769,21 +832,20 @@ def rms_norm_bwd(x, weight, dy, eps: float = 1e-5, z=None, gate: str = "none", d
     where it had a residual; dresidual is the gradient that reaches residual_out from elsewhere
     (added to dx).  Returns a dict of dx (the residual's gradient too), dweight (float32) and, with
     a gate, dz."""
-    torch = _torch()
-    desc = _norm_desc(x, weight, eps, z, gate, 0, ((dy, "dy"), (dresidual, "dresidual"),
-                                                   (dx, "dx"), (dz, "dz")))
+    plan = _norm_inputs(x, weight, eps, z, gate, 0, ((dy, "dy"), (dresidual, "dresidual"),
+                                                     (dx, "dx"), (dz, "dz")))
     if z is None and dz is not None:
         raise ValueError("dz goes with z")
     call = _Call(x, stream)
     g = dict(dx=call.empty(x.shape, x.dtype) if dx is None else dx,
-             dweight=call.empty(weight.shape, torch.float32))
+             dweight=call.empty(weight.shape, call.torch.float32))
     if z is not None:
         g["dz"] = call.empty(x.shape, x.dtype) if dz is None else dz
-    n = lib().ssd_rms_norm_bwd_workspace_size(ctypes.byref(desc))
-    if n == 0:
+    if plan.bwd_size == 0:   # the entry point says what it refuses
+        lib().ssd_rms_norm_bwd_workspace_size(plan.ref)
         raise SSDError(SSD_ERR_INVALID_ARG, last_error())
-    workspace = call.workspace(workspace, n)
-    call.run(lib().ssd_rms_norm_bwd, ctypes.byref(desc), _ptr(x), _ptr(z), _ptr(weight), _ptr(dy),
+    workspace = call.workspace(workspace, plan.bwd_size)
+    call.run(lib().ssd_rms_norm_bwd, plan.ref, _ptr(x), _ptr(z), _ptr(weight), _ptr(dy),
              _ptr(dresidual), _ptr(g["dx"]), _ptr(g.get("dz")), _ptr(g["dweight"]),
              _ptr(workspace), workspace.numel())
     return g
