@@ -10,19 +10,27 @@ namespace {
 // fast.
 constexpr int kChunkTokens = 24;
 
-bool chunked(const ssd_shape *s)
+enum class Path { kRecurrent, kChunk, kTc };
+
+Path forward_path(const ssd_shape *s)
 {
-    return delta_chunk_supported(s->dtype == SSD_BF16, (int)s->headdim, (int)s->dstate) &&
-           s->seqlen >= kChunkTokens;
+    const bool is_bf16 = s->dtype == SSD_BF16;
+    if (s->seqlen < kChunkTokens) return Path::kRecurrent;
+    if (delta_tc_supported(is_bf16, (int)s->headdim, (int)s->dstate)) return Path::kTc;
+    return delta_chunk_supported(is_bf16, (int)s->headdim, (int)s->dstate) ? Path::kChunk
+                                                                           : Path::kRecurrent;
 }
 
-// Bytes of the chunks' items over all heads.
-size_t items_bytes(const ssd_shape *s, int64_t chunks, bool for_backward)
-{
-    return (size_t)(s->batch * chunks * s->nheads) * DeltaItem::bytes(for_backward);
-}
+int64_t chunks_of(const ssd_shape *s, int tokens) { return (s->seqlen + tokens - 1) / tokens; }
 
-int64_t chunks_of(const ssd_shape *s) { return (s->seqlen + kDeltaChunk - 1) / kDeltaChunk; }
+// Tokens of a forward chunk, and the bytes of `chunks` of them over all heads.
+int path_tokens(Path p) { return p == Path::kTc ? kDeltaTcChunk : kDeltaChunk; }
+size_t items_bytes(const ssd_shape *s, Path p, int64_t chunks)
+{
+    const size_t items = (size_t)(s->batch * chunks * s->nheads);
+    return p == Path::kTc ? items * kDeltaTcItem
+                          : p == Path::kChunk ? items * DeltaItem::bytes(false) : 0;
+}
 
 ssd_status check_delta(const ssd_shape *s, const ssd_delta_options *o, bool need_seq)
 {
@@ -68,12 +76,13 @@ struct VarlenWs {
 VarlenWs varlen_ws(const ssd_shape *s, int nseq)
 {
     VarlenWs w;
-    w.slots = s->seqlen / kDeltaChunk + nseq;
+    const Path path = forward_path(s);
+    w.slots = s->seqlen / path_tokens(path) + nseq;
     w.status = 0;
     w.tab = 256;
     w.cstart = w.tab + api_round256((size_t)w.slots * sizeof(int2));
     w.items = w.cstart + api_round256((size_t)(nseq + 1) * sizeof(int32_t));
-    w.total = w.items + (chunked(s) ? items_bytes(s, w.slots, false) : 0);
+    w.total = w.items + items_bytes(s, path, w.slots);
     return w;
 }
 
@@ -102,7 +111,7 @@ struct BwdWs {
 BwdWs bwd_ws(const ssd_shape *s)
 {
     BwdWs w;
-    w.chunks = chunks_of(s);
+    w.chunks = chunks_of(s, kDeltaChunk);
     w.spans = (s->seqlen + 63) / 64;
     const size_t H = (size_t)s->nheads, PN = (size_t)(s->headdim * s->dstate);
     const size_t items = (size_t)(s->batch * w.chunks) * H, spans = (size_t)(s->batch * w.spans) * H;
@@ -176,7 +185,8 @@ extern "C" {
 size_t ssd_delta_rule_workspace_size(const ssd_shape *shape)
 {
     if (check_delta(shape, nullptr, true) != SSD_OK) return 0;
-    return 256 + (chunked(shape) ? items_bytes(shape, chunks_of(shape), false) : 0);
+    const Path path = forward_path(shape);
+    return 256 + items_bytes(shape, path, chunks_of(shape, path_tokens(path)));
 }
 
 ssd_status ssd_delta_rule_fwd(const ssd_shape *shape, const void *q, const void *k,
@@ -209,11 +219,15 @@ ssd_status ssd_delta_rule_fwd(const ssd_shape *shape, const void *q, const void 
     if (workspace_bytes < need)
         return api_fail(SSD_ERR_INVALID_ARG, "workspace too small: need %zu bytes, got %zu", need,
                         workspace_bytes);
-    if (chunked(&s)) {
-        char *items = static_cast<char *>(workspace) + 256;
-        e = launch_delta_prep(a, items, false, chunks_of(&s), nullptr, cst);
+    const Path path = forward_path(&s);
+    char *items = static_cast<char *>(workspace) + 256;
+    const int64_t chunks = chunks_of(&s, path_tokens(path));
+    if (path == Path::kTc) {
+        e = launch_delta_tc(a, items, chunks, nullptr, nullptr, static_cast<int *>(workspace), cst);
+    } else if (path == Path::kChunk) {
+        e = launch_delta_prep(a, items, false, chunks, nullptr, cst);
         if (e == cudaSuccess)
-            e = launch_delta_chain(a, nullptr, items, chunks_of(&s), nullptr, nullptr, nullptr, cst);
+            e = launch_delta_chain(a, nullptr, items, chunks, nullptr, nullptr, nullptr, cst);
     } else {
         e = launch_delta_recurrent(a, s.dtype == SSD_BF16, nullptr, cst);
     }
@@ -257,9 +271,12 @@ ssd_status ssd_delta_rule_varlen_fwd(const ssd_shape *shape, const void *q, cons
     int *status = reinterpret_cast<int *>(ws + w.status);
     int2 *tab = reinterpret_cast<int2 *>(ws + w.tab);
     int32_t *cstart = reinterpret_cast<int32_t *>(ws + w.cstart);
-    cudaError_t e = launch_build_chunk_table(cu_seqlens, nseq, a.L, kDeltaChunk, w.slots, tab,
+    const Path path = forward_path(shape);
+    cudaError_t e = launch_build_chunk_table(cu_seqlens, nseq, a.L, path_tokens(path), w.slots, tab,
                                              cstart, status, cst);
-    if (e == cudaSuccess && chunked(shape)) {
+    if (e == cudaSuccess && path == Path::kTc) {
+        e = launch_delta_tc(a, ws + w.items, w.slots, tab, cstart, status, cst);
+    } else if (e == cudaSuccess && path == Path::kChunk) {
         e = launch_delta_prep(a, ws + w.items, false, w.slots, tab, cst);
         if (e == cudaSuccess)
             e = launch_delta_chain(a, nullptr, ws + w.items, w.slots, tab, cstart, status, cst);

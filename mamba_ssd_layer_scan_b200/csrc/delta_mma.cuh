@@ -39,10 +39,18 @@ __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v 
 
 // x and y as bf16 pairs: hi the roundings, lo the roundings of what they leave.  hi + lo is x to
 // 2^-16 of it: products with an exact bf16 operand then keep float32's usual accuracy.
+__device__ __forceinline__ void split2(uint64_t xy, uint32_t &hi, uint32_t &lo)
+{
+    float x, y;
+    sm100::unpair(xy, x, y);
+    hi = sm100::pack_bf16x2(x, y);
+    sm100::unpair(sm100::fma2(sm100::pair(bf16_lo(hi), bf16_hi(hi)), sm100::pair(-1.f, -1.f), xy),
+                  x, y);
+    lo = sm100::pack_bf16x2(x, y);
+}
 __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo)
 {
-    hi = sm100::pack_bf16x2(x, y);
-    lo = sm100::pack_bf16x2(x - bf16_lo(hi), y - bf16_hi(hi));
+    split2(sm100::pair(x, y), hi, lo);
 }
 
 // The A operand made of two neighbouring D tiles.

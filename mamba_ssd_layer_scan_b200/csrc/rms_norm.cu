@@ -22,6 +22,8 @@
 namespace ssd {
 namespace {
 
+using namespace sm100;
+
 constexpr int kRowThreads = 256;   // CTA of the lanes-per-row variants
 constexpr int kMaxDim = 16384;
 constexpr int kMaxRowThreads = 512;
@@ -144,29 +146,6 @@ __device__ __forceinline__ float sigmoid(float z)
     return r;
 }
 
-// Two float32 operations in one instruction: x <- x y, and d + x y.
-__device__ __forceinline__ uint64_t pair(float x, float y)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ void unpair(uint64_t p, float &x, float &y)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t d)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(d));
-    return r;
-}
 // x <- x y for a thread's vector (y: another vector, or one factor), and the two halves of the sum
 // of squares.
 template <int VEC> __device__ __forceinline__ void times(float (&x)[VEC], const float (&y)[VEC])
@@ -258,7 +237,7 @@ template <typename T, int VEC, int NV, int TPR, int kOps> struct Walk {
         row = (int64_t)blockIdx.x * per_cta + sub;
 #pragma unroll
         for (int j = 0; j < NV; ++j) on[j] = (j * tpr + lane) * VEC < dim;
-        slot = sm100::smem_u32(ring) + threadIdx.x * 16;
+        slot = smem_u32(ring) + threadIdx.x * 16;
     }
     __device__ __forceinline__ int64_t at(int j) const
     {
