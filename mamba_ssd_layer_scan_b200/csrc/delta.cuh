@@ -35,7 +35,7 @@ bool delta_chunk_supported(bool is_bf16, int P, int N);
 // The chunked form on tcgen05 (delta_tc.cu): bf16, P and N 64 or 128.  `status` is the workspace's
 // status word, which it sets.
 constexpr int kDeltaTcChunk = 64;
-constexpr int kDeltaTcItem = 25 * 1024;   // bytes of the workspace per chunk and head
+constexpr int kDeltaTcItem = 19 * 1024;   // bytes of the workspace per chunk and head
 bool delta_tc_supported(bool is_bf16, int P, int N);
 cudaError_t launch_delta_tc(const DeltaArgs &a, char *items, int64_t nchunks, const int2 *tab,
                             const int32_t *cstart, int *status, cudaStream_t st);

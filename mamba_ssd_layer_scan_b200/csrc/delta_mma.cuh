@@ -53,6 +53,20 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     split2(sm100::pair(x, y), hi, lo);
 }
 
+// The two parts one at a time.
+__device__ __forceinline__ uint32_t round2(uint64_t xy)
+{
+    float x, y;
+    sm100::unpair(xy, x, y);
+    return sm100::pack_bf16x2(x, y);
+}
+__device__ __forceinline__ uint32_t rest2(uint64_t xy)
+{
+    uint32_t hi, lo;
+    split2(xy, hi, lo);
+    return lo;
+}
+
 // The A operand made of two neighbouring D tiles.
 __device__ __forceinline__ void split_a(const float (&t0)[4], const float (&t1)[4],
                                         uint32_t (&hi)[4], uint32_t (&lo)[4])

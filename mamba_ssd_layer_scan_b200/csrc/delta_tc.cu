@@ -31,17 +31,26 @@ constexpr float kLog2eLow = 1.9259629911266175e-8f;
 template <int I> struct Int { static constexpr int value = I; };
 
 // ---------------------------------------------------------------- the triangles
-// An item, per chunk and head: Inv in two parts, Att, and the factors -ek, sw, eq (64 floats each)
-// and E (four times).
-constexpr int kItemAtt = 2 * kTile, kItemVec = 3 * kTile, kVecFloats = 3 * kC + 4;
+// A triangle, 64 x 64 bf16 in 6 KB: columns 0-31 of all rows, then columns 32-63 of rows 32-63, in
+// rows of 64 bytes, 64-byte swizzled.  An item, per chunk and head: Inv in two parts, Att, and the
+// factors -ek, sw, eq (64 floats each) and E (four times).
+constexpr int kMat = 6 * 1024, kMatRight = 4 * 1024;
+constexpr int kItemAtt = 2 * kMat, kItemVec = 3 * kMat, kVecFloats = 3 * kC + 4;
 constexpr int kItem = kDeltaTcItem, kItemUsed = kItemVec + kVecFloats * 4;
-static_assert(kItemUsed <= kItem && kItemUsed % 16 == 0, "an item");
+static_assert(kItemUsed <= kItem && kItemUsed % 16 == 0 && kItem % 1024 == 0, "an item");
+// Byte offset of the 16-byte piece `c` (8 columns) of row `r` of a triangle.
+__device__ __forceinline__ uint32_t tri_at(int r, int c)
+{
+    return (c < 4 ? r * 64 : kMatRight + (r - 32) * 64) + (((c ^ (r >> 1)) & 3) << 4);
+}
 
-constexpr int kPrepThreads = 128, kPrepQuad = 4;
+constexpr int kPrepWarps = 4, kPrepThreads = 2 * kPrepWarps * 32, kPrepQuad = 4;
 // what the builders need of a head: log2(e) cs and its low part, both negated, kb, w
 constexpr int kCs = 0, kCl = kC, kKb = 2 * kC, kW = 3 * kC, kGateFloats = 4 * kC;
-constexpr int kPrepGates = 2 * 3 * kTile, kPrepNorms = kPrepGates + kPrepQuad * kGateFloats * 4,
+constexpr int kPrepGates = 2 * 3 * kMat,   // K and Q lie there first
+              kPrepNorms = kPrepGates + 2 * kPrepQuad * kGateFloats * 4,
               kPrepSmem = kPrepNorms + 2 * kC * 4;
+static_assert(kPrepGates >= 4 * kTile, "K and Q of 128 columns");
 
 // Byte offset of 16-byte piece `c` of row `r` in a tile of 128-byte rows, 128-byte swizzled.
 __device__ __forceinline__ uint32_t sw_at(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
@@ -209,7 +218,7 @@ __device__ __forceinline__ void build_rows(const float (&g)[8][4], int b, const 
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const uint64_t v = mul2(mul2(pair(g[n][2 * y], g[n][2 * y + 1]), w), u[y]);
-                    const uint32_t at = tri + sw_at(r[y], n) + j0 * 2;
+                    const uint32_t at = tri + tri_at(r[y], n) + j0 * 2;
                     if constexpr (kAtt) {
                         float x, z;
                         unpair(v, x, z);
@@ -218,7 +227,7 @@ __device__ __forceinline__ void build_rows(const float (&g)[8][4], int b, const 
                         uint32_t hi, lo;
                         split2(v, hi, lo);
                         sts32(at, hi);
-                        sts32(at + kTile, lo);
+                        sts32(at + kMat, lo);
                     }
                 }
             }
@@ -240,9 +249,9 @@ __device__ __forceinline__ void build_rows(const float (&g)[8][4], int b, const 
                     x = j < end ? x : 0.f;
                     z = j + 1 < end ? z : 0.f;
                     if constexpr (kAtt)
-                        sts32(tri + kItemAtt + sw_at(r[y], n) + j0 * 2, pack_bf16x2(x, z));
+                        sts32(tri + kItemAtt + tri_at(r[y], n) + j0 * 2, pack_bf16x2(x, z));
                     else
-                        sts64(tri + n % 2 * kTile + sw_at(r[y], 2 * bb + j0 / 4) + j0 % 4 * 4, x, z);
+                        sts64(tri + n % 2 * kMat + tri_at(r[y], 2 * bb + j0 / 4) + j0 % 4 * 4, x, z);
                 }
             }
         }
@@ -264,15 +273,15 @@ __device__ __forceinline__ void solve_head(uint32_t tri, int blk, int id)
         for (int s = 0; s < kB; ++s) {
             if (s > skip) break;
             uint32_t ah[4], al[4], bh[4], bl[4];
-            const uint32_t at = tri + sw_at(m0 + lane % 16, r1 / 8 + s * 2 + lane / 16);
+            const uint32_t at = tri + tri_at(m0 + lane % 16, r1 / 8 + s * 2 + lane / 16);
             ldsm4(ah, at);
-            ldsm4(al, at + kTile);
+            ldsm4(al, at + kMat);
 #pragma unroll
             for (int n = 0; n < kB; ++n) {
-                const uint32_t bt = tri + sw_at(r1 + s * 16 + lane % 8 + (lane / 8 & 1) * 8,
+                const uint32_t bt = tri + tri_at(r1 + s * 16 + lane % 8 + (lane / 8 & 1) * 8,
                                                 c0 / 8 + n * 2 + lane / 16);
                 ldsm4_trans(bh, bt);
-                ldsm4_trans(bl, bt + kTile);
+                ldsm4_trans(bl, bt + kMat);
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     mma_16816(Y[2 * n + m], ah, bh[2 * m], bh[2 * m + 1]);
@@ -287,10 +296,10 @@ __device__ __forceinline__ void solve_head(uint32_t tri, int blk, int id)
             split_a(Y[2 * s], Y[2 * s + 1], ah, al);
 #pragma unroll
             for (int n = 0; n <= s; ++n) {
-                const uint32_t bt = tri + sw_at(c0 + s * 16 + lane % 8 + (lane / 8 & 1) * 8,
+                const uint32_t bt = tri + tri_at(c0 + s * 16 + lane % 8 + (lane / 8 & 1) * 8,
                                                 c0 / 8 + n * 2 + lane / 16);
                 ldsm4_trans(bh, bt);
-                ldsm4_trans(bl, bt + kTile);
+                ldsm4_trans(bl, bt + kMat);
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     mma_16816(Z[2 * n + m], ah, bh[2 * m], bh[2 * m + 1]);
@@ -308,9 +317,9 @@ __device__ __forceinline__ void solve_head(uint32_t tri, int blk, int id)
                 uint32_t hi, lo;
                 split2(-Z[n][2 * k], -Z[n][2 * k + 1], hi, lo);
                 const uint32_t at =
-                    tri + sw_at(m0 + lane / 4 + k * 8, c0 / 8 + n) + lane % 4 * 4;
+                    tri + tri_at(m0 + lane / 4 + k * 8, c0 / 8 + n) + lane % 4 * 4;
                 sts32(at, hi);
-                sts32(at + kTile, lo);
+                sts32(at + kMat, lo);
             }
     };
     {
@@ -323,7 +332,7 @@ __device__ __forceinline__ void solve_head(uint32_t tri, int blk, int id)
 #pragma unroll
             for (int k = 0; k < m; k += 4) {
                 const float4 A =
-                    lds128(tri + k / 8 * kTile + sw_at(r0 + m, own * 2 + k / 4 % 2));
+                    lds128(tri + k / 8 * kMat + tri_at(r0 + m, own * 2 + k / 4 % 2));
                 s0 = fmaf(-A.x, v[k], s0);
                 if (k + 1 < m) s1 = fmaf(-A.y, v[k + 1], s1);
                 if (k + 2 < m) s0 = fmaf(-A.z, v[k + 2], s0);
@@ -340,9 +349,9 @@ __device__ __forceinline__ void solve_head(uint32_t tri, int blk, int id)
             uint32_t hi, lo;
             split2(odd ? other : v[m], odd ? v[m + 1] : other, hi, lo);
             const uint32_t at =
-                tri + sw_at(r0 + m + odd, own * 2 + col / 8) + (lane % 8 & ~1) * 2;
+                tri + tri_at(r0 + m + odd, own * 2 + col / 8) + (lane % 8 & ~1) * 2;
             sts32(at, hi);
-            sts32(at + kTile, lo);
+            sts32(at + kMat, lo);
         }
         __syncwarp();
         float Z[4][4] = {};   // the block of 16 below the diagonal, inside this block of 32
@@ -357,11 +366,12 @@ __device__ __forceinline__ void solve_head(uint32_t tri, int blk, int id)
     store_merged(Int<2>{}, 32 + blk * 16, 0, Z);
 }
 
-// grid: chunks * batch * G * runs of `run_heads` heads; 4 warps.  Warp w has 16 rows of the products
-// with the keys, block w of A and block 3 - w of Att (in registers for all heads of the run), and
-// half of a head's Inv.
+// grid: chunks * batch * G * runs of `run_heads` heads; two groups of 4 warps.  A warp has 16 rows of
+// the products with the keys in registers for all heads of the run: of K K^T in the first group,
+// which builds A and turns it into Inv, of Q K^T in the second, which builds Att and makes the
+// factors of the next four heads meanwhile.
 template <int N>
-__global__ void __launch_bounds__(kPrepThreads, 4)
+__global__ void __launch_bounds__(kPrepThreads, 3)
 delta_tc_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, int run_heads, const int2 *tab,
                      int *status)
 {
@@ -378,7 +388,8 @@ delta_tc_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, int run_he
     int len;
     chunk_span(tab, c, kC, a.L, t0, len);
     if (len <= 0) return;
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32 % kPrepWarps;
+    const bool att = tid >= kPrepWarps * 32;
     const int64_t row0 = b * a.L + t0;
     const uint32_t base = smem_u32(smem);
     float *norms = reinterpret_cast<float *>(smem + kPrepNorms);   // of keys; of queries, times scale
@@ -400,80 +411,87 @@ delta_tc_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, int run_he
         cp_wait<0>();
         __syncthreads();
     }
-    {   // a row per thread: keys, then queries
-        float v = tid < kC ? 1.f : a.scale;
+    {   // half a row per thread: keys, then queries
+        const int row = tid / 2;
+        float ss = 0.f;
         if (a.l2norm) {
-            uint64_t ss[2] = {};
+            uint64_t sum[2] = {};
 #pragma unroll
-            for (int j = 0; j < N / 8; ++j) {
-                const float4 w = lds128(base + (j / 8 * 2 + tid / kC) * kTile + sw_at(tid % kC, j % 8));
+            for (int j = 0; j < N / 16; ++j) {
+                const int col = tid % 2 * (N / 16) + j;
+                const float4 w =
+                    lds128(base + (col / 8 * 2 + row / kC) * kTile + sw_at(row % kC, col % 8));
                 const float f[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t u = __float_as_uint(f[k]);
                     const uint64_t y = pair(bf16_lo(u), bf16_hi(u));
-                    ss[k % 2] = fma2(y, y, ss[k % 2]);
+                    sum[k % 2] = fma2(y, y, sum[k % 2]);
                 }
             }
             float y, z;
-            unpair(add2(ss[0], ss[1]), y, z);
-            v *= rsqrtf(y + z + kL2Eps);
+            unpair(add2(sum[0], sum[1]), y, z);
+            ss = y + z;
         }
-        norms[tid] = v;
+        ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+        const float r = a.l2norm ? rsqrtf(ss + kL2Eps) : 1.f;
+        if (tid % 2 == 0) norms[row] = row < kC ? r : r * a.scale;
     }
-    float gk[8][4] = {}, gq[8][4] = {};
-    const int bk = warp, bq = 3 - warp;
+    // the later blocks have more columns: spread over the SM's quarters
+    const int blk = att ? kPrepWarps - 1 - warp : warp;
+    float g[8][4] = {};
 #pragma unroll
     for (int s = 0; s < N / 16; ++s) {
         const uint32_t tile = base + s / 4 * 2 * kTile;
-        uint32_t fk[4], fq[4], fb[4];
-        ldsm4(fk, tile + sw_at(bk * 16 + lane % 16, s % 4 * 2 + lane / 16));
-        ldsm4(fq, tile + kTile + sw_at(bq * 16 + lane % 16, s % 4 * 2 + lane / 16));
+        uint32_t fa[4], fb[4];
+        ldsm4(fa, tile + att * kTile + sw_at(blk * 16 + lane % 16, s % 4 * 2 + lane / 16));
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-            if (n > bk && n > bq) break;
+            if (n > blk) break;
             ldsm4(fb, tile + sw_at(n * 16 + lane % 8 + lane / 16 * 8, s % 4 * 2 + (lane / 8 & 1)));
-            if (n <= bk) {
-                mma_16816(gk[2 * n], fk, fb[0], fb[1]);
-                mma_16816(gk[2 * n + 1], fk, fb[2], fb[3]);
-            }
-            if (n <= bq) {
-                mma_16816(gq[2 * n], fq, fb[0], fb[1]);
-                mma_16816(gq[2 * n + 1], fq, fb[2], fb[3]);
-            }
+            mma_16816(g[2 * n], fa, fb[0], fb[1]);
+            mma_16816(g[2 * n + 1], fa, fb[2], fb[3]);
         }
     }
     __syncthreads();   // K's and Q's place is the triangles' now
 
-    const int h_end = min(hpg, (run + 1) * run_heads);
-    for (int hq = run * run_heads; hq < h_end; hq += kPrepQuad) {
-        char *item = items + ((b * nchunks + c) * a.H + grp * hpg + hq) * (int64_t)kItem;
-        if (hq + warp < h_end)
-            head_gates(a, row0, len, grp * hpg + hq + warp, norms,
-                       reinterpret_cast<float *>(smem + kPrepGates) + warp * kGateFloats,
-                       reinterpret_cast<float *>(item + warp * (int64_t)kItem + kItemVec));
-        for (int p = 0; p < kPrepQuad; p += 2) {
-            const int here = min(2, h_end - hq - p);   // heads of this pair
-            if (here <= 0) break;
-            if (tid == 0) bulk_store_wait();
-            __syncthreads();
-            for (int x = 0; x < here; ++x) {
-                const uint32_t gates = base + kPrepGates + (p + x) * kGateFloats * 4;
-                build_rows<false>(gk, bk, norms, gates, base + x * 3 * kTile);
-                build_rows<true>(gq, bq, norms, gates, base + x * 3 * kTile);
-            }
-            __syncthreads();
-            if (warp / 2 < here) solve_head(base + warp / 2 * 3 * kTile, warp % 2, 1 + warp / 2);
-            fence_async_smem();
-            __syncthreads();
-            if (tid == 0)
-                for (int x = 0; x < here; ++x)
-                    bulk_store(item + (p + x) * (int64_t)kItem, base + x * 3 * kTile, 3 * kTile);
+    const int h_begin = run * run_heads, h_end = min(hpg, h_begin + run_heads);
+    const int64_t item0 = (b * nchunks + c) * a.H + grp * hpg;
+    auto gates_of = [&](int hq) { return kPrepGates + ((hq - h_begin) & kPrepQuad) * kGateFloats * 4; };
+    auto make_gates = [&](int hq) {   // of heads hq .. hq + 3: a warp each
+        const int hl = hq + warp;
+        if (hl < h_end)
+            head_gates(a, row0, len, grp * hpg + hl, norms,
+                       reinterpret_cast<float *>(smem + gates_of(hq)) + warp * kGateFloats,
+                       reinterpret_cast<float *>(items + (item0 + hl) * kItem + kItemVec));
+    };
+    if (att) make_gates(h_begin);
+    for (int hp = h_begin; hp < h_end; hp += 2) {
+        const int hq = h_begin + ((hp - h_begin) & ~(kPrepQuad - 1));
+        const int here = min(2, h_end - hp);   // heads of this pair
+        if (tid == 0) bulk_store_wait();
+        __syncthreads();
+        const uint32_t gates = base + gates_of(hq) + (hp - hq) * kGateFloats * 4;
+        for (int x = 0; x < here; ++x) {
+            if (att) build_rows<true>(g, blk, norms, gates + x * kGateFloats * 4, base + x * 3 * kMat);
+            else build_rows<false>(g, blk, norms, gates + x * kGateFloats * 4, base + x * 3 * kMat);
         }
+        if (att) {
+            if (hp > hq || hp + 2 >= h_end) {
+                if (hq + kPrepQuad < h_end) make_gates(hq + kPrepQuad);
+            }
+        } else {
+            named_bar_sync(3, kPrepWarps * 32);
+            if (warp / 2 < here) solve_head(base + warp / 2 * 3 * kMat, warp % 2, 1 + warp / 2);
+        }
+        fence_async_smem();
+        __syncthreads();
+        if (tid == 0)
+            for (int x = 0; x < here; ++x)
+                bulk_store(items + (item0 + hp + x) * kItem, base + x * 3 * kMat, 3 * kMat);
     }
     if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
-
 
 // ---------------------------------------------------------------- the chain
 constexpr int kRowWarps = 8, kMma = kRowWarps, kLoadKq = kMma + 1, kLoadV = kMma + 2;   // and items
@@ -641,7 +659,6 @@ __device__ __forceinline__ void row_warps(const DeltaArgs &a, TcBars &bar, uint3
         tmem_st_wait();
         tc_fence_before();
         arrive_warp(&bar.r_ready);
-        if (c > 0) store_out(c - 1);   // while W is on its way
 
         if (!wait_all(&bar.w_done, c & 1, abort)) return;
         tc_fence_after();
@@ -669,6 +686,7 @@ __device__ __forceinline__ void row_warps(const DeltaArgs &a, TcBars &bar, uint3
         tmem_st_wait();
         tc_fence_before();
         arrive_warp(&bar.w_ready);
+        if (c > 0) store_out(c - 1);   // while the state's update is on its way
     }
     if (!take_update(nchunks - 1)) return;
     if (a.final_state && here) {
@@ -704,7 +722,7 @@ __device__ __forceinline__ void issue_products(TcBars &bar, uint32_t base, uint3
     const uint64_t identd = smem_desc_sw128(base + L::kIdent, 0, 1024);
     const uint64_t kq0 = smem_desc_sw128(base, 0, 1024);
     const uint64_t kc0 = smem_desc_sw128(base, L::kHalf, 1024);
-    const uint64_t tri0 = smem_desc_sw128(base + L::kTris, 0, 1024);
+    const uint64_t tri0 = smem_desc_sw64(base + L::kTris, 512);
 
     auto products_v = [&](int c) {   // V^T, 16 tokens at a time, through the identity
         if (!wait_all(&bar.v_full[c & 1], (c >> 1) & 1, abort)) return false;
@@ -742,12 +760,12 @@ __device__ __forceinline__ void issue_products(TcBars &bar, uint32_t base, uint3
         if (!wait_all(&bar.r_ready, c & 1, abort)) return;
         tc_fence_after();
         // a triangle: tokens 16 k on take the written values of tokens 16 k .. 16 k + 15
-        auto with_tri = [&](uint32_t d, uint32_t op, int step, uint64_t tile, bool first) {
+        auto with_tri = [&](uint32_t d, uint32_t op, int step, uint64_t mat, bool first) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 warp_mma_bf16_ts(on, tmem + d + k * 16, tmem + op + k / 2 * step + k % 2 * 8,
-                            tile + k * ((16 * 128 + 32) >> 4),
-                            idesc_bf16_f32(128, 64 - 16 * k, false, false), !first || k > 0);
+                                 mat + ((k / 2 * kMatRight + k % 2 * (16 * 64 + 32)) >> 4),
+                                 idesc_bf16_f32(128, 64 - 16 * k, false, false), !first || k > 0);
         };
         const uint64_t tris = tri0 + buf * (HP * kItem >> 4);
 #pragma unroll
@@ -757,7 +775,7 @@ __device__ __forceinline__ void issue_products(TcBars &bar, uint32_t base, uint3
             const uint64_t tri = tris + x * (kItem >> 4);
             with_tri(d, kColOp, 16, tri, true);
             with_tri(d, kColOp + 32, 16, tri, false);
-            with_tri(d, kColOp, 16, tri + (kTile >> 4), false);
+            with_tri(d, kColOp, 16, tri + (kMat >> 4), false);
         }
         warp_mma_commit(on, &bar.w_done);
 
@@ -991,7 +1009,7 @@ cudaError_t launch_delta_tc(const DeltaArgs &a, char *items, int64_t nchunks, co
     // where the launch would leave SMs empty
     int run = hpg < 16 ? (int)hpg : 16;
     auto ctas = [&] { return nchunks * batch * a.G * ((hpg + run - 1) / run); };
-    while (run > kPrepQuad && ctas() < 592) run = (run + 1) / 2;
+    while (run > kPrepQuad && ctas() < 2 * 444) run = (run + 1) / 2;
     auto prep = [&](auto kern) {
         cudaError_t e =
             cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrepSmem);

@@ -388,6 +388,13 @@ __host__ __device__ constexpr uint64_t smem_desc_sw128(uint32_t saddr, uint32_t 
            ((uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// K-major rows of 64 bytes, 64-byte swizzled (piece j of row r at j ^ (r / 2 % 4)).
+__host__ __device__ constexpr uint64_t smem_desc_sw64(uint32_t saddr, uint32_t sbo_bytes)
+{
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32) |
+           (1ull << 46) | (4ull << 61);
+}
+
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn, bool b_mn)
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) |
