@@ -33,6 +33,8 @@ using namespace sm100;
 constexpr int C = kDeltaChunk;
 constexpr int kPrepWarps = 4;
 constexpr int kPrepHeads = 16;     // heads of a group per CTA of the prep kernel
+constexpr int kLoadWarps = 2;      // of a CTA of the chains, behind the warps that compute
+constexpr int kMaxRows = 112;      // of a CTA of the chains: leaves a thread 224 registers
 constexpr float kMinDecay = -200.f;    // exp of it is 0 in float32
 constexpr float kMinBeta = 1e-20f;
 
@@ -232,7 +234,7 @@ struct ChainSlice {
     }
 };
 
-// Issues the copies of chunk c into the stage at shared address s.
+// Issues the copies of chunk c into the stage at shared address s: the load warps.
 template <int N, bool kBwd>
 __device__ __forceinline__ void load_stage(const DeltaArgs &a, const ChainStage &lay,
                                            const ChainSlice &w, const char *items,
@@ -243,7 +245,8 @@ __device__ __forceinline__ void load_stage(const DeltaArgs &a, const ChainStage 
     int len;
     chunk_span(tab, c, C, a.L, t0, len);
     const int64_t row0 = w.b * a.L + t0;
-    const int tid = threadIdx.x, nthr = blockDim.x;
+    const int tid = threadIdx.x % (kLoadWarps * 32);
+    constexpr int nthr = kLoadWarps * 32;
     const bf16 *kg = static_cast<const bf16 *>(a.k) + (row0 * a.G + w.g) * N;
     const bf16 *qg = static_cast<const bf16 *>(a.q) + (row0 * a.G + w.g) * N;
     for (int i = tid; i < C * (N / 8); i += nthr) {
@@ -362,7 +365,7 @@ template <int kDots> __device__ __forceinline__ void fold_tokens(float (&v)[kDot
 // grid: (sequences * H / heads * P / rows).  kBwd: the forward once more for the backward, which
 // keeps the state every 64 tokens, W, and the dot products of o and its gradient instead of o.
 template <int N, bool kBwd>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__((kMaxRows / 16 + kLoadWarps) * 32)
 delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64_t nchunks,
                    const int2 *tab, const int32_t *cstart, const int *status, int heads, int rows)
 {
@@ -378,28 +381,29 @@ delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64
     const int64_t b = slice.b, seq = slice.seq;
     const int64_t c_begin = cstart ? cstart[seq] : 0, c_end = cstart ? cstart[seq + 1] : nchunks;
 
+    const uint32_t base = smem_u32(smem);
+    if (hl >= heads) {   // the load warps: a chunk ahead of the others
+        for (int64_t c = c_begin; c <= c_end; ++c) {
+            if (c < c_end)
+                load_stage<N, kBwd>(a, lay, slice, items, w.dout, nchunks, tab, c,
+                                    base + ((c - c_begin) & 1) * lay.total);
+            cp_commit();
+            cp_wait<0>();
+            __syncthreads();   // chunk c has arrived; chunk c - 1 is done with
+        }
+        return;
+    }
     float S[NT][4] = {};
     const int64_t pn = (int64_t)(p0 + lane / 4) * N + lane % 4 * 2;   // this lane, in a P x N state
     const int64_t srow = (seq * a.H + h) * P * N + pn;
     if (a.init) load_acc<N>(a.init + srow, S);
 
-    const uint32_t base = smem_u32(smem);
-    auto load = [&](int64_t c, int stage) {
-        load_stage<N, kBwd>(a, lay, slice, items, w.dout, nchunks, tab, c,
-                            base + stage * lay.total);
-    };
-
-    if (c_begin < c_end) load(c_begin, 0);
-    cp_commit();
     // fragment addresses inside a stage
     const int row_nn = lane % 8 + lane / 16 * 8, col_nn = (lane / 8 & 1) * 16;   // rows on n
     const int row_kk = lane % 8 + (lane / 8 & 1) * 8, col_kk = lane / 16 * 16;   // rows on k
     for (int64_t c = c_begin; c < c_end; ++c) {
         const int stage = (int)(c - c_begin) & 1;
-        cp_wait<0>();
         __syncthreads();   // this chunk has arrived; everyone is done with the other stage
-        if (c + 1 < c_end) load(c + 1, stage ^ 1);
-        cp_commit();
 
         const uint32_t ks = base + stage * lay.total, qs = ks + C * lay.kpitch;
         const uint32_t vs = qs + C * lay.kpitch + hl * lay.head;
@@ -559,7 +563,7 @@ delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64
             store_tokens(O, vs + pl * 2, lay.vpitch, vaddr, static_cast<bf16 *>(a.o) + tokens,
                          (int64_t)a.H * P, len, lane);
     }
-    cp_wait<0>();
+    __syncthreads();   // the load warps' last one
     if (kBwd)
         store_acc<N>(w.states + ((b * (w.n64 + 1) + w.n64) * a.H + h) * P * N + pn, S);
     else if (a.final_state)
@@ -576,7 +580,7 @@ delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64
 // products of each token's dV with V and W, every 64 tokens dS' (bf16) and <dS', S'>, and dS of
 // the initial state.
 template <int N>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__((kMaxRows / 16 + kLoadWarps) * 32)
 delta_adjoint_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64_t nchunks,
                      int heads, int rows)
 {
@@ -590,26 +594,28 @@ delta_adjoint_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int
     const int p0 = slice.pb + pl, h = slice.h0 + hl;
     const int64_t b = slice.b;
 
+    const uint32_t base = smem_u32(smem);
+    if (hl >= heads) {   // the load warps
+        for (int64_t c = nchunks - 1; c >= -1; --c) {
+            if (c >= 0)
+                load_stage<N, true>(a, lay, slice, items, w.dout, nchunks, nullptr, c,
+                                    base + ((nchunks - 1 - c) & 1) * lay.total);
+            cp_commit();
+            cp_wait<0>();
+            __syncthreads();
+        }
+        return;
+    }
     float D[NT][4] = {};
     const int64_t pn = (int64_t)(p0 + lane / 4) * N + lane % 4 * 2;
     const int64_t srow = (b * a.H + h) * P * N + pn;
     if (w.dfinal) load_acc<N>(w.dfinal + srow, D);
 
-    const uint32_t base = smem_u32(smem);
-    auto load = [&](int64_t c, int stage) {
-        load_stage<N, true>(a, lay, slice, items, w.dout, nchunks, nullptr, c,
-                            base + stage * lay.total);
-    };
-    load(nchunks - 1, 0);
-    cp_commit();
     const int row_nn = lane % 8 + lane / 16 * 8, col_nn = (lane / 8 & 1) * 16;   // rows on n
     const int row_kk = lane % 8 + (lane / 8 & 1) * 8, col_kk = lane / 16 * 16;   // rows on k
     for (int64_t c = nchunks - 1; c >= 0; --c) {
         const int stage = (int)(nchunks - 1 - c) & 1;
-        cp_wait<0>();
         __syncthreads();
-        if (c > 0) load(c - 1, stage ^ 1);
-        cp_commit();
 
         const uint32_t ks = base + stage * lay.total, qs = ks + C * lay.kpitch;
         const uint32_t vs = qs + C * lay.kpitch + hl * lay.head;
@@ -775,14 +781,14 @@ delta_adjoint_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int
             }
         }
     }
-    cp_wait<0>();
+    __syncthreads();   // the load warps' last one
     if (w.dinit) store_acc<N>(w.dinit + srow, D);
 }
 
-// Rows of a head per CTA: all of them, or fewer where the launch would leave SMs empty.
+// Rows of a head per CTA: all of them (half of 128), or fewer where the launch would leave SMs empty.
 int chain_rows(const DeltaArgs &a, int64_t nseq)
 {
-    int rows = a.P;
+    int rows = a.P > kMaxRows ? a.P / 2 : a.P;
     while (nseq * a.H * (a.P / rows) < 148 && rows % 32 == 0) rows /= 2;
     return rows;
 }
@@ -817,7 +823,7 @@ cudaError_t launch_delta_chain(const DeltaArgs &a, const DeltaBwd *bwd, const ch
     const int64_t nseq = cstart ? a.nseq : a.batch;
     const int heads = 1, rows = chain_rows(a, nseq);
     const unsigned grid = (unsigned)(nseq * (a.H / heads) * (a.P / rows));
-    const unsigned threads = (unsigned)(heads * rows / 16 * 32);
+    const unsigned threads = (unsigned)((heads * rows / 16 + kLoadWarps) * 32);
     const int smem = 2 * ChainStage(rows, a.N, heads, bwd != nullptr).total;
     const DeltaBwd w = bwd ? *bwd : DeltaBwd{};
     auto go = [&](auto kern) {
@@ -835,7 +841,7 @@ cudaError_t launch_delta_adjoint(const DeltaArgs &a, const DeltaBwd &w, const ch
 {
     const int heads = 1, rows = chain_rows(a, a.batch);
     const unsigned grid = (unsigned)(a.batch * (a.H / heads) * (a.P / rows));
-    const unsigned threads = (unsigned)(heads * rows / 16 * 32);
+    const unsigned threads = (unsigned)((heads * rows / 16 + kLoadWarps) * 32);
     const int smem = 2 * ChainStage(rows, a.N, heads, true).total;
     auto go = [&](auto kern) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
