@@ -357,8 +357,14 @@ ssd_status ssd_chunk_scan_fwd_static_status(void *stream);
  *                (batch, nheads, headdim, dstate) float32, both nullable (zeros; not written).
  *                final_state may be init_state.  o must not alias any input.
  *   workspace    ssd_delta_rule_workspace_size bytes (0: invalid shape), 256-byte aligned, with
- *                the scan's rules: contents do not matter, concurrent calls use distinct ones.
+ *                the scan's rules: contents do not matter, concurrent calls use distinct ones, and
+ *                ssd_workspace_status() reads the status word that the last call left.
  * q, k, v, o and the states must be 16-byte aligned.  batch == 0 or seqlen == 0 is valid.
+ *
+ * bf16 with dstate 64 or 128 and headdim a multiple of 16 runs in chunks of 32 or 64 tokens, on
+ * tcgen05 for headdim 64 and 128 once there is enough to do; the state keeps float32's usual
+ * accuracy.  A NaN or infinity at a token reaches, in its own sequence and head (a key's or query's:
+ * its group's heads), the later tokens and the outputs of its chunk.
  */
 typedef struct {
     float scale;          /* of the output; usually 1 / sqrt(dstate) */

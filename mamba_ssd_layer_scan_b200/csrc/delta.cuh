@@ -7,6 +7,39 @@ namespace ssd {
 
 constexpr float kL2Eps = 1e-6f;   // under the root of q's and k's norms
 
+// Kernels of one call that follow one another: a kernel launched with launch_after() may start while
+// the one before it still runs, and reads nothing of it before wait_before() returns (every CTA
+// calls it); let_next_start() in the earlier kernel allows it.
+__device__ __forceinline__ void wait_before()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_start()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                         Args... args)
+{
+    if (smem > 40 * 1024) {   // with the static part this may pass 48 KB
+        const cudaError_t e =
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
+}
+
 struct DeltaArgs {
     const void *q, *k, *v;      // (batch, L, G, N), same, (batch, L, H, P)
     const float *g, *beta;      // (batch, L, H); g nullable (no decay)
@@ -19,6 +52,7 @@ struct DeltaArgs {
     int l2norm;
     const int32_t *cu;          // packed sequences (batch 1): nseq + 1 offsets, else null
     int nseq;
+    int *clear;                 // a status word that the call's first kernel clears; nullable
 };
 
 // The recurrence token by token, any supported shape and type, state rows in registers.
@@ -32,11 +66,11 @@ cudaError_t launch_delta_recurrent(const DeltaArgs &a, bool is_bf16, const int *
 constexpr int kDeltaChunk = 32;
 bool delta_chunk_supported(bool is_bf16, int P, int N);
 
-// The chunked form on tcgen05 (delta_tc.cu): bf16, P and N 64 or 128.  `status` is the workspace's
-// status word, which it sets.
+// The chunked form on tcgen05 (delta_tc.cu): bf16, P and N 64 or 128.  A bounded wait that gives up
+// sets a bit of `status`, the workspace's status word.
 constexpr int kDeltaTcChunk = 64;
 constexpr int kDeltaTcItem = 19 * 1024;   // bytes of the workspace per chunk and head
-bool delta_tc_supported(bool is_bf16, int P, int N);
+bool delta_tc_supported(int P, int N);
 cudaError_t launch_delta_tc(const DeltaArgs &a, char *items, int64_t nchunks, const int2 *tab,
                             const int32_t *cstart, int *status, cudaStream_t st);
 

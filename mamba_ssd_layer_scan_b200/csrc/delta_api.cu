@@ -6,19 +6,26 @@
 namespace ssd {
 namespace {
 
-// The chunked kernels from this many tokens on: below it the token recurrence, one launch, is as
-// fast.
-constexpr int kChunkTokens = 24;
+// The kernels of a forward pass.  Below kChunkTokens the token recurrence, one launch, is as fast as
+// the chunked kernels.  Of these the warp-level ones (16 state rows to a warp) are ahead while each
+// warp has an SM to itself, by 5 us at any length (8 heads of 64, N 128, us: 129 tokens 16 against
+// 21, 2048 tokens 94 against 103; 37 heads 17 against 21, 105 against 109), and for sequences of up
+// to 64 tokens (8 x 80 heads: 34 against 38; of 128 tokens 55 against 48); with more to do the
+// tcgen05 ones are (80 heads, 2048 tokens: 125 against 182; 8 x 80 heads 442 against 643).
+constexpr int kChunkTokens = 24, kTcTokens = 64;
+constexpr int64_t kTcRows = 148 * 16;
 
 enum class Path { kRecurrent, kChunk, kTc };
 
-Path forward_path(const ssd_shape *s)
+Path forward_path(const ssd_shape *s, int64_t nseq)
 {
     const bool is_bf16 = s->dtype == SSD_BF16;
-    if (s->seqlen < kChunkTokens) return Path::kRecurrent;
-    if (delta_tc_supported(is_bf16, (int)s->headdim, (int)s->dstate)) return Path::kTc;
-    return delta_chunk_supported(is_bf16, (int)s->headdim, (int)s->dstate) ? Path::kChunk
-                                                                           : Path::kRecurrent;
+    if (s->seqlen < kChunkTokens ||
+        !delta_chunk_supported(is_bf16, (int)s->headdim, (int)s->dstate)) return Path::kRecurrent;
+    const int64_t tokens = s->batch * s->seqlen;   // over all sequences
+    return delta_tc_supported((int)s->headdim, (int)s->dstate) && tokens > nseq * kTcTokens &&
+                   nseq * s->nheads * s->headdim > kTcRows
+               ? Path::kTc : Path::kChunk;
 }
 
 int64_t chunks_of(const ssd_shape *s, int tokens) { return (s->seqlen + tokens - 1) / tokens; }
@@ -76,7 +83,7 @@ struct VarlenWs {
 VarlenWs varlen_ws(const ssd_shape *s, int nseq)
 {
     VarlenWs w;
-    const Path path = forward_path(s);
+    const Path path = forward_path(s, nseq);
     w.slots = s->seqlen / path_tokens(path) + nseq;
     w.status = 0;
     w.tab = 256;
@@ -185,7 +192,7 @@ extern "C" {
 size_t ssd_delta_rule_workspace_size(const ssd_shape *shape)
 {
     if (check_delta(shape, nullptr, true) != SSD_OK) return 0;
-    const Path path = forward_path(shape);
+    const Path path = forward_path(shape, shape->batch);
     return 256 + items_bytes(shape, path, chunks_of(shape, path_tokens(path)));
 }
 
@@ -219,7 +226,8 @@ ssd_status ssd_delta_rule_fwd(const ssd_shape *shape, const void *q, const void 
     if (workspace_bytes < need)
         return api_fail(SSD_ERR_INVALID_ARG, "workspace too small: need %zu bytes, got %zu", need,
                         workspace_bytes);
-    const Path path = forward_path(&s);
+    a.clear = static_cast<int *>(workspace);
+    const Path path = forward_path(&s, s.batch);
     char *items = static_cast<char *>(workspace) + 256;
     const int64_t chunks = chunks_of(&s, path_tokens(path));
     if (path == Path::kTc) {
@@ -271,7 +279,7 @@ ssd_status ssd_delta_rule_varlen_fwd(const ssd_shape *shape, const void *q, cons
     int *status = reinterpret_cast<int *>(ws + w.status);
     int2 *tab = reinterpret_cast<int2 *>(ws + w.tab);
     int32_t *cstart = reinterpret_cast<int32_t *>(ws + w.cstart);
-    const Path path = forward_path(shape);
+    const Path path = forward_path(shape, nseq);
     cudaError_t e = launch_build_chunk_table(cu_seqlens, nseq, a.L, path_tokens(path), w.slots, tab,
                                              cstart, status, cst);
     if (e == cudaSuccess && path == Path::kTc) {
@@ -328,6 +336,7 @@ ssd_status ssd_delta_rule_bwd(const ssd_shape *shape, const void *q, const void 
     if (workspace_bytes < l.total)
         return api_fail(SSD_ERR_INVALID_ARG, "workspace too small: need %zu bytes, got %zu",
                         l.total, workspace_bytes);
+    a.clear = static_cast<int *>(workspace);
     char *ws = static_cast<char *>(workspace);
     auto f32 = [&](size_t at) { return reinterpret_cast<float *>(ws + at); };
     DeltaBwd w = {};

@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(kGradThreads)
 delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
 {
     extern __shared__ __align__(128) char smem[];
+    wait_before();
     constexpr int NT = N / 16;   // n8 tiles of a warp's half of the columns
     const GradSmem lay(a.P, N);
     const int P = a.P, H = a.H, hpg = a.H / a.G;
@@ -260,6 +261,7 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
             }
         }
     }
+    let_next_start();
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -279,6 +281,8 @@ __global__ void __launch_bounds__(256)
 delta_qk_kernel(const DeltaArgs a, const DeltaBwd w, int64_t rows)
 {
     constexpr int V = N / 32;
+    let_next_start();
+    wait_before();
     const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;   // (b, t, g)
     const int lane = threadIdx.x % 32;
     if (row >= rows) return;
@@ -317,6 +321,7 @@ delta_qk_kernel(const DeltaArgs a, const DeltaBwd w, int64_t rows)
 __global__ void __launch_bounds__(256)
 delta_gate_kernel(const DeltaArgs a, const DeltaBwd w, int64_t nchunks, int64_t spans)
 {
+    wait_before();
     const int64_t item = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;   // (b, span, h)
     const int lane = threadIdx.x % 32;
     if (item >= spans) return;
@@ -365,23 +370,16 @@ cudaError_t launch_delta_grads(const DeltaArgs &a, const DeltaBwd &w, int64_t nc
 {
     const int smem = GradSmem(a.P, a.N).total;
     const dim3 grid((unsigned)w.n64, (unsigned)a.batch, (unsigned)(a.G * w.runs));
-    auto go = [&](auto kern) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        kern<<<grid, kGradThreads, smem, st>>>(a, w);
-        return cudaGetLastError();
-    };
-    cudaError_t e = a.N == 128 ? go(delta_grad_kernel<128>) : go(delta_grad_kernel<64>);
+    cudaError_t e =
+        launch_after(a.N == 128 ? delta_grad_kernel<128> : delta_grad_kernel<64>, grid, kGradThreads,
+                     smem, st, a, w);
     if (e != cudaSuccess) return e;
     const int64_t rows = a.batch * a.L * a.G, spans = a.batch * w.n64 * a.H;
-    if (a.N == 128)
-        delta_qk_kernel<128><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(a, w, rows);
-    else
-        delta_qk_kernel<64><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(a, w, rows);
-    e = cudaGetLastError();
+    e = launch_after(a.N == 128 ? delta_qk_kernel<128> : delta_qk_kernel<64>,
+                     (unsigned)((rows + 7) / 8), 256, 0, st, a, w, rows);
     if (e != cudaSuccess) return e;
-    delta_gate_kernel<<<(unsigned)((spans + 7) / 8), 256, 0, st>>>(a, w, nchunks, spans);
-    return cudaGetLastError();
+    return launch_after(delta_gate_kernel, (unsigned)((spans + 7) / 8), 256, 0, st, a, w, nchunks,
+                        spans);
 }
 
 }  // namespace ssd

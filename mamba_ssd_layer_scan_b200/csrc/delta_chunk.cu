@@ -32,7 +32,7 @@ using namespace sm100;
 
 constexpr int C = kDeltaChunk;
 constexpr int kPrepWarps = 4;
-constexpr int kPrepHeads = 16;     // heads of a group per CTA of the prep kernel
+constexpr int kPrepHeads = 16;     // most heads of a group per CTA of the prep kernel
 constexpr int kLoadWarps = 2;      // of a CTA of the chains, behind the warps that compute
 constexpr int kMaxRows = 112;      // of a CTA of the chains: leaves a thread 224 registers
 constexpr float kMinDecay = -200.f;    // exp of it is 0 in float32
@@ -56,7 +56,7 @@ __device__ __forceinline__ void two_sum(float a, float b, float &s, float &err)
 // from 0, where the backward divides by it (a token of beta 1e-20 writes nothing either).
 template <int N, bool kBwd>
 __global__ void __launch_bounds__(kPrepWarps * 32)
-delta_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, const int2 *tab)
+delta_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, const int2 *tab, int run_heads)
 {
     constexpr int kPitch = N + 8;   // elements; 16 bytes more than a row: no bank conflicts
     __shared__ __align__(16) bf16 ks[C * kPitch], qs[C * kPitch];
@@ -64,8 +64,9 @@ delta_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, const int2 *t
     __shared__ __align__(16) float As[kPrepWarps][C][C + 4];
     __shared__ float rqs[C];
 
+    if (blockIdx.x + blockIdx.y + blockIdx.z + threadIdx.x == 0 && a.clear) *a.clear = 0;
     const int64_t c = blockIdx.x, b = blockIdx.y;
-    const int hpg = a.H / a.G, runs = (hpg + kPrepHeads - 1) / kPrepHeads;
+    const int hpg = a.H / a.G, runs = (hpg + run_heads - 1) / run_heads;
     const int g = blockIdx.z / runs, run = blockIdx.z % runs;
     int64_t t0;
     int len;
@@ -127,8 +128,8 @@ delta_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, const int2 *t
     const float rk = a.l2norm ? rsqrtf(kk[lane][lane] + kL2Eps) : 1.f;
     const float rq = (a.l2norm ? rqs[lane] : 1.f) * a.scale;
     float (*A)[C + 4] = As[warp];
-    const int h_end = min(hpg, (run + 1) * kPrepHeads);
-    for (int hl = run * kPrepHeads + warp; hl < h_end; hl += kPrepWarps) {
+    const int h_end = min(hpg, (run + 1) * run_heads);
+    for (int hl = run * run_heads + warp; hl < h_end; hl += kPrepWarps) {
         const int h = g * hpg + hl;
         const int64_t at = (row0 + lane) * a.H + h;
         float gt = on && a.g ? a.g[at] : 0.f;
@@ -370,7 +371,10 @@ delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64
                    const int2 *tab, const int32_t *cstart, const int *status, int heads, int rows)
 {
     extern __shared__ __align__(128) char smem[];
-    if (status && *status) return;
+    if (status && *status) {
+        wait_before();
+        return;
+    }
     constexpr int NT = N / 8;
     const int P = a.P;
     const ChainStage lay(rows, N, heads, kBwd);
@@ -383,6 +387,7 @@ delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64
 
     const uint32_t base = smem_u32(smem);
     if (hl >= heads) {   // the load warps: a chunk ahead of the others
+        wait_before();   // the others read nothing of the kernel before
         for (int64_t c = c_begin; c <= c_end; ++c) {
             if (c < c_end)
                 load_stage<N, kBwd>(a, lay, slice, items, w.dout, nchunks, tab, c,
@@ -564,6 +569,7 @@ delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64
                          (int64_t)a.H * P, len, lane);
     }
     __syncthreads();   // the load warps' last one
+    let_next_start();
     if (kBwd)
         store_acc<N>(w.states + ((b * (w.n64 + 1) + w.n64) * a.H + h) * P * N + pn, S);
     else if (a.final_state)
@@ -585,6 +591,7 @@ delta_adjoint_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int
                      int heads, int rows)
 {
     extern __shared__ __align__(128) char smem[];
+    wait_before();
     constexpr int NT = N / 8;
     const int P = a.P;
     const ChainStage lay(rows, N, heads, true);
@@ -782,6 +789,7 @@ delta_adjoint_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int
         }
     }
     __syncthreads();   // the load warps' last one
+    let_next_start();
     if (w.dinit) store_acc<N>(w.dinit + srow, D);
 }
 
@@ -803,17 +811,21 @@ bool delta_chunk_supported(bool is_bf16, int P, int N)
 cudaError_t launch_delta_prep(const DeltaArgs &a, char *items, bool for_backward, int64_t nchunks,
                               const int2 *tab, cudaStream_t st)
 {
-    const int runs = (a.H / a.G + kPrepHeads - 1) / kPrepHeads;
-    const dim3 grid((unsigned)nchunks, (unsigned)(tab ? 1 : a.batch), (unsigned)(a.G * runs));
+    // fewer heads per CTA where the launch would leave SMs empty (at 1 x 64 tokens x 24 heads 16 heads
+    // to a CTA took 28 us, 4 of them 8)
+    const int64_t batch = tab ? 1 : a.batch, hpg = a.H / a.G;
+    int run = hpg < kPrepHeads ? (int)hpg : kPrepHeads;
+    auto runs = [&] { return (hpg + run - 1) / run; };
+    while (run > kPrepWarps && nchunks * batch * a.G * runs() < 592) run = (run + 1) / 2;
+    const dim3 grid((unsigned)nchunks, (unsigned)batch, (unsigned)(a.G * runs()));
     const dim3 block(kPrepWarps * 32);
-    if (a.N == 128) {
-        if (for_backward) delta_prep_kernel<128, true><<<grid, block, 0, st>>>(a, items, nchunks, tab);
-        else delta_prep_kernel<128, false><<<grid, block, 0, st>>>(a, items, nchunks, tab);
-    } else {
-        if (for_backward) delta_prep_kernel<64, true><<<grid, block, 0, st>>>(a, items, nchunks, tab);
-        else delta_prep_kernel<64, false><<<grid, block, 0, st>>>(a, items, nchunks, tab);
-    }
-    return cudaGetLastError();
+    auto go = [&](auto kern) {
+        kern<<<grid, block, 0, st>>>(a, items, nchunks, tab, run);
+        return cudaGetLastError();
+    };
+    if (a.N == 128)
+        return for_backward ? go(delta_prep_kernel<128, true>) : go(delta_prep_kernel<128, false>);
+    return for_backward ? go(delta_prep_kernel<64, true>) : go(delta_prep_kernel<64, false>);
 }
 
 cudaError_t launch_delta_chain(const DeltaArgs &a, const DeltaBwd *bwd, const char *items,
@@ -827,10 +839,7 @@ cudaError_t launch_delta_chain(const DeltaArgs &a, const DeltaBwd *bwd, const ch
     const int smem = 2 * ChainStage(rows, a.N, heads, bwd != nullptr).total;
     const DeltaBwd w = bwd ? *bwd : DeltaBwd{};
     auto go = [&](auto kern) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        kern<<<grid, threads, smem, st>>>(a, w, items, nchunks, tab, cstart, status, heads, rows);
-        return cudaGetLastError();
+        return launch_after(kern, grid, threads, smem, st, a, w, items, nchunks, tab, cstart, status, heads, rows);
     };
     if (bwd) return a.N == 128 ? go(delta_chain_kernel<128, true>) : go(delta_chain_kernel<64, true>);
     return a.N == 128 ? go(delta_chain_kernel<128, false>) : go(delta_chain_kernel<64, false>);
@@ -844,10 +853,7 @@ cudaError_t launch_delta_adjoint(const DeltaArgs &a, const DeltaBwd &w, const ch
     const unsigned threads = (unsigned)((heads * rows / 16 + kLoadWarps) * 32);
     const int smem = 2 * ChainStage(rows, a.N, heads, true).total;
     auto go = [&](auto kern) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        kern<<<grid, threads, smem, st>>>(a, w, items, nchunks, heads, rows);
-        return cudaGetLastError();
+        return launch_after(kern, grid, threads, smem, st, a, w, items, nchunks, heads, rows);
     };
     return a.N == 128 ? go(delta_adjoint_kernel<128>) : go(delta_adjoint_kernel<64>);
 }

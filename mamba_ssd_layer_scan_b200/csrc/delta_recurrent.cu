@@ -61,6 +61,7 @@ delta_recurrent_kernel(const DeltaArgs a, const int *status)
 {
     constexpr int N = 32 * V;
     if (status && *status) return;
+    if (a.clear && blockIdx.x + threadIdx.x == 0) *a.clear = 0;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int pblocks = (a.P + kRows * kWarps - 1) / (kRows * kWarps);
     const int h = (int)((blockIdx.x / pblocks) % a.H);

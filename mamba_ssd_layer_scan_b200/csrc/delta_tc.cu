@@ -107,19 +107,22 @@ __device__ __forceinline__ void two_sum(float a, float b, float &s, float &err)
     err = (a - (s - bb)) + (b - bb);
 }
 
-// The running sums of g of a head's chunk and the factors that come of them, a warp: `gates` for the
-// builders, `vec` (global) for the chain.  Lane l has tokens 2 l and 2 l + 1.
-__device__ __forceinline__ void head_gates(const DeltaArgs &a, int64_t row0, int len, int h,
-                                           const float *norms, float *gates, float *vec)
+// A head's gates in a chunk, a warp; lane l has tokens 2 l and 2 l + 1.  First the running sums of g
+// (times log2(e), hi + lo) and beta.
+struct Gates {
+    float hi[2], lo[2], beta[2];
+};
+__device__ __forceinline__ Gates sum_gates(const DeltaArgs &a, int64_t row0, int len, int h)
 {
     const int lane = threadIdx.x % 32, i = 2 * lane;
-    float g[2] = {}, beta[2] = {};
+    Gates s = {};
+    float g[2] = {};
 #pragma unroll
     for (int y = 0; y < 2; ++y)
         if (i + y < len) {
             const int64_t at = (row0 + i + y) * a.H + h;
             if (a.g) g[y] = a.g[at];
-            beta[y] = a.beta[at];
+            s.beta[y] = a.beta[at];
         }
 #pragma unroll
     for (int y = 0; y < 2; ++y) g[y] = g[y] < -200.f ? -200.f : g[y];
@@ -143,12 +146,20 @@ __device__ __forceinline__ void head_gates(const DeltaArgs &a, int64_t row0, int
     if (lane == 0) before = beforel = 0.f;
     two_sum(before, g[0], cs[0], cl[0]);
     cl[0] += beforel;
-    float hi[2], lo[2];
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {   // times log2(e), the product's rounding kept as well
-        hi[y] = cs[y] * kLog2e;
-        lo[y] = fmaf(cs[y], kLog2e, -hi[y]) + fmaf(cs[y], kLog2eLow, cl[y] * kLog2e);
+    for (int y = 0; y < 2; ++y) {   // the product's rounding kept as well
+        s.hi[y] = cs[y] * kLog2e;
+        s.lo[y] = fmaf(cs[y], kLog2e, -s.hi[y]) + fmaf(cs[y], kLog2eLow, cl[y] * kLog2e);
     }
+    return s;
+}
+// Then the factors that come of them: `gates` for the builders, `vec` (global) for the chain.
+__device__ __forceinline__ void make_factors(const Gates &s, int len, const float *norms, float *gates,
+                                             float *vec)
+{
+    const int lane = threadIdx.x % 32, i = 2 * lane;
+    const float(&hi)[2] = s.hi;
+    const float(&lo)[2] = s.lo;
     const float end = __shfl_sync(0xffffffffu, hi[1], 31);
     const float endl = __shfl_sync(0xffffffffu, lo[1], 31);
     // in the blocks below the diagonal exp(cs_i - cs_j) is taken by way of the last token of j's
@@ -160,7 +171,7 @@ __device__ __forceinline__ void head_gates(const DeltaArgs &a, int64_t row0, int
     for (int y = 0; y < 2; ++y) {
         const bool on = i + y < len;
         const float rk = norms[i + y], ex = ex2(hi[y] + lo[y]);
-        kb[y] = on ? rk * beta[y] : 0.f;
+        kb[y] = on ? rk * s.beta[y] : 0.f;
         ek[y] = on ? -ex * rk : 0.f;
         sw[y] = ex2((end - hi[y]) + (endl - lo[y])) * kb[y];
         eq[y] = on ? ex * norms[kC + i + y] : 0.f;
@@ -372,13 +383,13 @@ __device__ __forceinline__ void solve_head(uint32_t tri, int blk, int id)
 // factors of the next four heads meanwhile.
 template <int N>
 __global__ void __launch_bounds__(kPrepThreads, 3)
-delta_tc_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, int run_heads, const int2 *tab,
-                     int *status)
+delta_tc_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, int run_heads, const int2 *tab)
 {
     extern __shared__ __align__(128) char smem[];
+    let_next_start();
     const int hpg = a.H / a.G, runs = (hpg + run_heads - 1) / run_heads;
     int64_t id = blockIdx.x;
-    if (id == 0 && threadIdx.x == 0 && status) *status = 0;
+    if (id == 0 && threadIdx.x == 0 && a.clear) *a.clear = 0;
     const int run = (int)(id % runs);
     id /= runs;
     const int grp = (int)(id % a.G);
@@ -408,9 +419,12 @@ delta_tc_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, int run_he
             cp16(at + kTile, qg + off, on);
         }
         cp_commit();
-        cp_wait<0>();
-        __syncthreads();
     }
+    const int h_begin = run * run_heads, h_end = min(hpg, h_begin + run_heads);
+    Gates first = {};   // while the copies are on their way
+    if (att && h_begin + warp < h_end) first = sum_gates(a, row0, len, grp * hpg + h_begin + warp);
+    cp_wait<0>();
+    __syncthreads();
     {   // half a row per thread: keys, then queries
         const int row = tid / 2;
         float ss = 0.f;
@@ -455,17 +469,16 @@ delta_tc_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, int run_he
     }
     __syncthreads();   // K's and Q's place is the triangles' now
 
-    const int h_begin = run * run_heads, h_end = min(hpg, h_begin + run_heads);
     const int64_t item0 = (b * nchunks + c) * a.H + grp * hpg;
     auto gates_of = [&](int hq) { return kPrepGates + ((hq - h_begin) & kPrepQuad) * kGateFloats * 4; };
-    auto make_gates = [&](int hq) {   // of heads hq .. hq + 3: a warp each
+    auto make_gates = [&](int hq, const Gates &sums) {   // of heads hq .. hq + 3: a warp each
         const int hl = hq + warp;
         if (hl < h_end)
-            head_gates(a, row0, len, grp * hpg + hl, norms,
-                       reinterpret_cast<float *>(smem + gates_of(hq)) + warp * kGateFloats,
-                       reinterpret_cast<float *>(items + (item0 + hl) * kItem + kItemVec));
+            make_factors(sums, len, norms,
+                         reinterpret_cast<float *>(smem + gates_of(hq)) + warp * kGateFloats,
+                         reinterpret_cast<float *>(items + (item0 + hl) * kItem + kItemVec));
     };
-    if (att) make_gates(h_begin);
+    if (att) make_gates(h_begin, first);
     for (int hp = h_begin; hp < h_end; hp += 2) {
         const int hq = h_begin + ((hp - h_begin) & ~(kPrepQuad - 1));
         const int here = min(2, h_end - hp);   // heads of this pair
@@ -478,7 +491,9 @@ delta_tc_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, int run_he
         }
         if (att) {
             if (hp > hq || hp + 2 >= h_end) {
-                if (hq + kPrepQuad < h_end) make_gates(hq + kPrepQuad);
+                const int next = hq + kPrepQuad;
+                if (next + warp < h_end)
+                    make_gates(next, sum_gates(a, row0, len, grp * hpg + next + warp));
             }
         } else {
             named_bar_sync(3, kPrepWarps * 32);
@@ -867,6 +882,7 @@ __device__ __forceinline__ void load_items(const DeltaArgs &a, TcBars &bar, char
                                            int heads)
 {
     using L = TcSmem<N, HP>;
+    wait_before();   // only this thread reads what the first kernel wrote
     for (int c = 0; c < nchunks; ++c) {
         const int buf = c & 1;
         if (c >= 2 && !mbar_wait(&bar.tri_empty[buf], ((c >> 1) - 1) & 1, &bar.abort)) return;
@@ -887,7 +903,10 @@ delta_tc_kernel(const DeltaArgs a, const char *items, int64_t nchunks_all, const
     constexpr int HP = 128 / P;
     using L = TcSmem<N, HP>;
     extern __shared__ char raw[];
-    if (cstart && *status) return;   // inconsistent offsets
+    if (cstart && *status) {   // inconsistent offsets
+        wait_before();
+        return;
+    }
     char *smem = reinterpret_cast<char *>(
         (reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     TcBars &bar = *reinterpret_cast<TcBars *>(smem + L::kBars);
@@ -926,6 +945,7 @@ delta_tc_kernel(const DeltaArgs a, const char *items, int64_t nchunks_all, const
             for (int i = tid; i < heads * P * N; i += kTcThreads)
                 a.final_state[at + i] = a.init ? a.init[at + i] : 0.f;
         }
+        wait_before();
         return;
     }
     if (tid == 0) {
@@ -996,10 +1016,7 @@ delta_tc_kernel(const DeltaArgs a, const char *items, int64_t nchunks_all, const
 
 }  // namespace
 
-bool delta_tc_supported(bool is_bf16, int P, int N)
-{
-    return is_bf16 && (P == 64 || P == 128) && (N == 64 || N == 128);
-}
+bool delta_tc_supported(int P, int N) { return (P == 64 || P == 128) && (N == 64 || N == 128); }
 
 cudaError_t launch_delta_tc(const DeltaArgs &a, char *items, int64_t nchunks, const int2 *tab,
                             const int32_t *cstart, int *status, cudaStream_t st)
@@ -1014,8 +1031,7 @@ cudaError_t launch_delta_tc(const DeltaArgs &a, char *items, int64_t nchunks, co
         cudaError_t e =
             cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrepSmem);
         if (e != cudaSuccess) return e;
-        kern<<<(unsigned)ctas(), kPrepThreads, kPrepSmem, st>>>(a, items, nchunks, run, tab,
-                                                              tab ? nullptr : status);
+        kern<<<(unsigned)ctas(), kPrepThreads, kPrepSmem, st>>>(a, items, nchunks, run, tab);
         return cudaGetLastError();
     };
     cudaError_t e = a.N == 128 ? prep(delta_tc_prep_kernel<128>) : prep(delta_tc_prep_kernel<64>);
@@ -1023,11 +1039,8 @@ cudaError_t launch_delta_tc(const DeltaArgs &a, char *items, int64_t nchunks, co
     const int hp = 128 / a.P;
     const unsigned grid = (unsigned)((a.cu ? a.nseq : a.batch) * a.G * ((hpg + hp - 1) / hp));
     auto go = [&](auto kern, int smem) {
-        smem += 1024;   // to an address that is a multiple of 1024
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        kern<<<grid, kTcThreads, smem, st>>>(a, items, nchunks, cstart, status);
-        return cudaGetLastError();
+        // to an address that is a multiple of 1024
+        return launch_after(kern, grid, kTcThreads, smem + 1024, st, a, items, nchunks, cstart, status);
     };
     if (a.P == 64)
         return a.N == 128 ? go(delta_tc_kernel<128, 64>, TcSmem<128, 2>::kTotal)
