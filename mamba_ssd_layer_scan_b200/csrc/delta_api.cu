@@ -123,14 +123,21 @@ BwdWs bwd_ws(const ssd_shape *s)
     const size_t H = (size_t)s->nheads, PN = (size_t)(s->headdim * s->dstate);
     const size_t items = (size_t)(s->batch * w.chunks) * H, spans = (size_t)(s->batch * w.spans) * H;
     const size_t tiles = (size_t)s->headdim / 16, tokens = (size_t)(s->batch * s->seqlen);
-    // up to eight heads of a group per CTA of the gradients' kernel, whose sums stay in
-    // registers; fewer where the launch would leave SMs empty
-    const int hpg = (int)(s->nheads / s->ngroups);
-    w.run_heads = hpg < 8 ? hpg : 8;
-    auto runs = [&] { return (hpg + w.run_heads - 1) / w.run_heads; };
-    while (w.run_heads > 1 && s->batch * w.spans * s->ngroups * runs() < 296)
-        w.run_heads = (w.run_heads + 1) / 2;
-    w.runs = runs();
+    // heads of a group per CTA of the gradients' kernel, whose sums stay in registers: what takes the
+    // fewest turns of a head (one more for a CTA's start) on 148 SMs with one or two CTAs each
+    const int64_t hpg = s->nheads / s->ngroups, slots = s->headdim <= 64 ? 296 : 148;
+    const int64_t spans_groups = s->batch * w.spans * s->ngroups;
+    int64_t best = 0;
+    w.run_heads = 1;
+    for (int64_t n = 1; n <= 8 && n <= hpg; ++n) {
+        const int64_t ctas = spans_groups * ((hpg + n - 1) / n);
+        const int64_t turns = (ctas + slots - 1) / slots * (n + 1);
+        if (n == 1 || turns <= best) {
+            best = turns;
+            w.run_heads = (int)n;
+        }
+    }
+    w.runs = (int)((hpg + w.run_heads - 1) / w.run_heads);
     size_t at = 256;
     auto take = [&](size_t bytes) {
         const size_t here = at;

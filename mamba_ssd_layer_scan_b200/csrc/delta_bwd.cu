@@ -30,10 +30,12 @@ using namespace sm100;
 constexpr int kSpan = 64;
 constexpr int kGradThreads = 256;
 
+// Tiles of 128- or 256-byte rows, 16-byte piece c of row r at piece c ^ (r % 8): no bank conflicts, and
+// two CTAs to an SM for P = 64.
 struct GradSmem {
-    int kpitch, vpitch, mpitch, k, q, dout, w, dv, s, ds, m1, m2, vec, total;
-    __host__ __device__ GradSmem(int P, int N)
-        : kpitch(N * 2 + 16), vpitch(P * 2 + 16), mpitch(kSpan * 2 + 16)
+    static constexpr int mpitch = kSpan * 2;
+    int kpitch, vpitch, k, q, dout, w, dv, s, ds, m1, m2, vec, total;
+    __host__ __device__ GradSmem(int P, int N) : kpitch(N * 2), vpitch(P <= 64 ? 128 : 256)
     {
         k = 0;
         q = k + kSpan * kpitch;
@@ -45,13 +47,17 @@ struct GradSmem {
         m1 = ds + P * kpitch;
         m2 = m1 + kSpan * mpitch;
         vec = m2 + kSpan * mpitch;
-        total = vec + 8 * kSpan * 4;
+        total = vec + 7 * kSpan * 4;
     }
 };
+__device__ __forceinline__ uint32_t swizzled(int row, int pitch, int piece)
+{
+    return row * pitch + ((piece ^ (row & 7)) << 4);
+}
 
 // grid: (spans, batch, G * runs); 8 warps
 template <int N>
-__global__ void __launch_bounds__(kGradThreads)
+__global__ void __launch_bounds__(kGradThreads, 2)
 delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
 {
     extern __shared__ __align__(128) char smem[];
@@ -76,8 +82,8 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
         const int r = i / (N / 8), col = i % (N / 8);
         const bool on = r < len;
         const int64_t off = on ? (int64_t)r * a.G * N + col * 8 : 0;
-        cp16(base + lay.k + r * lay.kpitch + col * 16, kg + off, on);
-        cp16(base + lay.q + r * lay.kpitch + col * 16, qg + off, on);
+        cp16(base + lay.k + swizzled(r, lay.kpitch, col), kg + off, on);
+        cp16(base + lay.q + swizzled(r, lay.kpitch, col), qg + off, on);
     }
     cp_commit();
     cp_wait<0>();
@@ -86,8 +92,9 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
         const int r = tid / 4;
         float kk = 0.f, qq = 0.f;
         for (int i = tid % 4 * 2; i < N; i += 8) {
-            const uint32_t x = *reinterpret_cast<const uint32_t *>(smem + lay.k + r * lay.kpitch + i * 2);
-            const uint32_t y = *reinterpret_cast<const uint32_t *>(smem + lay.q + r * lay.kpitch + i * 2);
+            const uint32_t at = swizzled(r, lay.kpitch, i / 8) + i % 8 * 2;
+            const uint32_t x = *reinterpret_cast<const uint32_t *>(smem + lay.k + at);
+            const uint32_t y = *reinterpret_cast<const uint32_t *>(smem + lay.q + at);
             kk = fmaf(bf16_lo(x), bf16_lo(x), fmaf(bf16_hi(x), bf16_hi(x), kk));
             qq = fmaf(bf16_lo(y), bf16_lo(y), fmaf(bf16_hi(y), bf16_hi(y), qq));
         }
@@ -103,9 +110,10 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
     }
 
     float dq[NT][4] = {}, dk[NT][4] = {};
-    const int row_nn = lane % 8 + lane / 16 * 8, col_nn = (lane / 8 & 1) * 16;   // rows on n
-    const int row_kk = lane % 8 + (lane / 8 & 1) * 8, col_kk = lane / 16 * 16;   // rows on k
-    const int row_a = lane % 16, col_a = lane / 16 * 16;                         // A, rows on m
+    // the row and piece of a fragment's address that are this lane's (rows on n, on k; A)
+    const int row_nn = lane % 8 + lane / 16 * 8, col_nn = lane / 8 & 1;
+    const int row_kk = lane % 8 + (lane / 8 & 1) * 8, col_kk = lane / 16;
+    const int row_a = lane % 16, col_a = lane / 16;
     const int h_end = min(hpg, (run + 1) * w.run_heads);
     for (int hl = run * w.run_heads; hl < h_end; ++hl) {
         const int h = g * hpg + hl;
@@ -116,14 +124,14 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
             const int r = i / pieces, col = i % pieces;
             const bool on = r < len;
             const int64_t off = vat + (on ? (int64_t)r * H * P + col * 8 : 0);
-            const uint32_t at = r * lay.vpitch + col * 16;
+            const uint32_t at = swizzled(r, lay.vpitch, col);
             cp16(base + lay.dout + at, w.dout + off, on);
             cp16(base + lay.w + at, w.w + off, on);
             cp16(base + lay.dv + at, w.dv + off, on);
         }
         const bf16 *dsg = w.dstates + ((b * w.n64 + span) * H + h) * P * N;
         for (int i = tid; i < P * (N / 8); i += kGradThreads)
-            cp16(base + lay.ds + i / (N / 8) * lay.kpitch + i % (N / 8) * 16, dsg + i * 8, true);
+            cp16(base + lay.ds + swizzled(i / (N / 8), lay.kpitch, i % (N / 8)), dsg + i * 8, true);
         cp_commit();
         const float *sg = w.states + ((b * (w.n64 + 1) + span) * H + h) * P * N;
         for (int i = tid; i < P * (N / 8); i += kGradThreads) {   // rounded to the operand's bf16
@@ -134,7 +142,8 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
             o.y = pack_bf16x2(u.z, u.w);
             o.z = pack_bf16x2(v.x, v.y);
             o.w = pack_bf16x2(v.z, v.w);
-            *reinterpret_cast<uint4 *>(smem + lay.s + i / (N / 8) * lay.kpitch + i % (N / 8) * 16) = o;
+            *reinterpret_cast<uint4 *>(smem + lay.s +
+                                       swizzled(i / (N / 8), lay.kpitch, i % (N / 8))) = o;
         }
         if (warp == 0) {   // the span's decays: lane has tokens lane and lane + 32
             float gt[2], beta[2];
@@ -175,11 +184,11 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
             float acc[8][4] = {};
             for (int s = 0; s < P / 16; ++s) {
                 uint32_t fa[4], fb[4];
-                ldsm4(fa, rows + (mt + row_a) * lay.vpitch + s * 32 + col_a);
+                ldsm4(fa, rows + swizzled(mt + row_a, lay.vpitch, s * 2 + col_a));
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     if (n * 16 > mt) break;
-                    ldsm4(fb, base + lay.w + (n * 16 + row_nn) * lay.vpitch + s * 32 + col_nn);
+                    ldsm4(fb, base + lay.w + swizzled(n * 16 + row_nn, lay.vpitch, s * 2 + col_nn));
                     mma_16816(acc[2 * n], fa, fb[0], fb[1]);
                     mma_16816(acc[2 * n + 1], fa, fb[2], fb[3]);
                 }
@@ -195,7 +204,7 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
                     const float x = on0 ? acc[n][2 * r] * f * __expf(ci - cs[j]) * kb[j] : 0.f;
                     const float y =
                         on1 ? acc[n][2 * r + 1] * f * __expf(ci - cs[j + 1]) * kb[j + 1] : 0.f;
-                    *reinterpret_cast<uint32_t *>(smem + out + i * lay.mpitch + j * 2) =
+                    *reinterpret_cast<uint32_t *>(smem + out + swizzled(i, lay.mpitch, n) + j % 8 * 2) =
                         pack_bf16x2(x, y);
                 }
             }
@@ -208,11 +217,11 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
             float acc[NT][4] = {};
             for (int s = 0; s < P / 16; ++s) {
                 uint32_t fa[4], fb[4];
-                ldsm4(fa, base + x + (mt + row_a) * lay.vpitch + s * 32 + col_a);
+                ldsm4(fa, base + x + swizzled(mt + row_a, lay.vpitch, s * 2 + col_a));
 #pragma unroll
                 for (int n = 0; n < NT / 2; ++n) {
-                    ldsm4_trans(fb, base + st + (s * 16 + row_kk) * lay.kpitch + nh * N +
-                                        n * 32 + col_kk);
+                    ldsm4_trans(fb, base + st + swizzled(s * 16 + row_kk, lay.kpitch,
+                                                         nh * N / 16 + n * 2 + col_kk));
                     mma_16816(acc[2 * n], fa, fb[0], fb[1]);
                     mma_16816(acc[2 * n + 1], fa, fb[2], fb[3]);
                 }
@@ -235,8 +244,8 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
             uint32_t fb[4];
 #pragma unroll
             for (int n = 0; n < NT / 2; ++n) {
-                ldsm4_trans(fb, base + rows + (s * 16 + row_kk) * lay.kpitch + nh * N + n * 32 +
-                                    col_kk);
+                ldsm4_trans(fb, base + rows + swizzled(s * 16 + row_kk, lay.kpitch,
+                                                       nh * N / 16 + n * 2 + col_kk));
                 mma_16816(to[2 * n], fa, fb[0], fb[1]);
                 mma_16816(to[2 * n + 1], fa, fb[2], fb[3]);
             }
@@ -244,17 +253,17 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
         for (int s = 0; s < 4; ++s) {
             uint32_t fa[4];
             if (s * 16 <= mt) {   // tokens up to these
-                ldsm4(fa, base + lay.m1 + (mt + row_a) * lay.mpitch + s * 32 + col_a);
+                ldsm4(fa, base + lay.m1 + swizzled(mt + row_a, lay.mpitch, s * 2 + col_a));
                 with_rows(fa, lay.k, s, dq);
-                ldsm4(fa, base + lay.m2 + (mt + row_a) * lay.mpitch + s * 32 + col_a);
+                ldsm4(fa, base + lay.m2 + swizzled(mt + row_a, lay.mpitch, s * 2 + col_a));
 #pragma unroll
                 for (int r = 0; r < 4; ++r) fa[r] ^= 0x80008000u;
                 with_rows(fa, lay.k, s, dk);
             }
             if (s * 16 >= mt) {   // tokens from these on: transposed
-                ldsm4_trans(fa, base + lay.m1 + (s * 16 + row_nn) * lay.mpitch + mt * 2 + col_nn);
+                ldsm4_trans(fa, base + lay.m1 + swizzled(s * 16 + row_nn, lay.mpitch, mt / 8 + col_nn));
                 with_rows(fa, lay.q, s, dk);
-                ldsm4_trans(fa, base + lay.m2 + (s * 16 + row_nn) * lay.mpitch + mt * 2 + col_nn);
+                ldsm4_trans(fa, base + lay.m2 + swizzled(s * 16 + row_nn, lay.mpitch, mt / 8 + col_nn));
 #pragma unroll
                 for (int r = 0; r < 4; ++r) fa[r] ^= 0x80008000u;
                 with_rows(fa, lay.k, s, dk);
