@@ -100,7 +100,7 @@ struct DeltaBwd {
     float *wfrag;          // W in accumulator layout, per (batch, chunk, H, tile): 16 x 32
     bf16 *w;               // (batch, L, H, P): W
     float *dot_oo, *dot_vv, *dot_vw;   // (batch, chunk, H, tile, 32): <dO, O>, <dV, V>, <dV, W>
-    float *dot_ss;         // (batch, n64, H, tile): <dS', S'>
+    float *dot_ss;         // (batch, n64 + 1, H, tile): <dS, S> at the start, then behind each span
     float *dq_part, *dk_part;          // (batch, L, G * runs, N)
     int runs;              // runs of heads per group, `run_heads` each (the last may be shorter)
     int run_heads;

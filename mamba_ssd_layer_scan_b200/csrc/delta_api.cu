@@ -152,7 +152,7 @@ BwdWs bwd_ws(const ssd_shape *s)
     w.dot_oo = take(items * tiles * kDeltaChunk * 4);
     w.dot_vv = take(items * tiles * kDeltaChunk * 4);
     w.dot_vw = take(items * tiles * kDeltaChunk * 4);
-    w.dot_ss = take(spans * tiles * 4);
+    w.dot_ss = take((spans + (size_t)s->batch * H) * tiles * 4);
     w.dq = take(tokens * (size_t)(s->ngroups * w.runs) * (size_t)s->dstate * 4);
     w.dk = take(tokens * (size_t)(s->ngroups * w.runs) * (size_t)s->dstate * 4);
     w.total = at;

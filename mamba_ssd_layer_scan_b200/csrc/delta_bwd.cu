@@ -12,13 +12,15 @@
 // with eq = e rq scale, ek = e rk, sw = (E / e) rk beta.  The gradients of the stored rows follow
 // from those of the normalised ones, y = q rq: dq = t - y (y . t), t = rq d(y).
 //
-// The decay's gradient at a token is <dS, S> behind it less what the token itself writes; within a
-// span it telescopes:
+// The decay's gradient at a token is <dS, S> before it, S having decayed; within a span of n tokens it
+// telescopes from either end, with x_s = <dO_s, O_s> - <dV_s, V_s>:
 //
-//     dg_t = <dS', S'> + sum over s >= t in the span of (<dO_s, O_s> - <dV_s, V_s>)
+//     dg_t = <dS', S'> + sum over s >= t of x_s = <dS, S> - sum over s < t of x_s
 //     dbeta_t = <dV_t, W_t> / beta_t
 //
-// where the dot products come from the chains in float32; spans of 64 tokens keep the sums short.
+// where the dot products come from the chains in float32.  The errors of the two sums add up over
+// n - t and t terms that partly cancel; weighted by t / n and (n - t) / n they give 0.6 of the first
+// one's error alone (7e-6 for 1.2e-5 of dg, 2-norm, at 2 x 2048 x 24 heads).
 #include "delta.cuh"
 #include "delta_mma.cuh"
 
@@ -350,16 +352,27 @@ delta_gate_kernel(const DeltaArgs a, const DeltaBwd w, int64_t nchunks, int64_t 
             }
         }
     }
-    for (int i = 0; i < tiles; ++i) ss += w.dot_ss[item * tiles + i];
+    const float *at_begin = w.dot_ss + ((b * (w.n64 + 1) + span) * a.H + h) * tiles;
+    const float *at_end = at_begin + (int64_t)a.H * tiles;
+    float begin = 0.f;
+    for (int i = 0; i < tiles; ++i) {
+        begin += at_begin[i];
+        ss += at_end[i];
+    }
     const float d1 = oo[1] - vv[1], d0 = oo[0] - vv[0];
-    float sum = d0 + d1;   // of this lane's tokens and all behind them
+    float sum = d0 + d1, before = d0 + d1;   // of this lane's tokens and all behind, or before, them
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const float dn = __shfl_down_sync(0xffffffffu, sum, o);
+        const float up = __shfl_up_sync(0xffffffffu, before, o);
         if (lane + o < 32) sum += dn;
+        if (lane >= o) before += up;
     }
-    const float behind = __shfl_down_sync(0xffffffffu, sum, 1);
-    const float after = ss + (lane < 31 ? behind : 0.f);
+    const float left = a.L - span * kSpan < kSpan ? (float)(a.L - span * kSpan) : (float)kSpan;
+    float behind = __shfl_down_sync(0xffffffffu, sum, 1);   // from token 2 l + 2 on
+    before = __shfl_up_sync(0xffffffffu, before, 1);        // up to token 2 l - 1
+    if (lane == 31) behind = 0.f;
+    if (lane == 0) before = 0.f;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const int64_t t = span * kSpan + lane * 2 + x;
@@ -368,7 +381,10 @@ delta_gate_kernel(const DeltaArgs a, const DeltaBwd w, int64_t nchunks, int64_t 
         float beta = a.beta[at];
         if (fabsf(beta) < 1e-20f) beta = 1e-20f;   // as the chains took it
         w.dbeta[at] = vw[x] / beta;
-        if (w.dg) w.dg[at] = after + d1 + (x == 0 ? d0 : 0.f);
+        const float from_end = ss + (behind + (x == 0 ? d0 + d1 : d1));
+        const float from_begin = begin - (x == 0 ? before : before + d0);
+        const float f = (float)(lane * 2 + x) / left;
+        if (w.dg) w.dg[at] = fmaf(f, from_end - from_begin, from_begin);
     }
 }
 

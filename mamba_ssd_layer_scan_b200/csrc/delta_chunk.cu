@@ -651,7 +651,8 @@ delta_adjoint_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
-            if (lane == 0) w.dot_ss[span * (P / 16) + p0 / 16] = f;
+            if (lane == 0)
+                w.dot_ss[((b * (w.n64 + 1) + c / 2 + 1) * a.H + h) * (P / 16) + p0 / 16] = f;
         }
 
         // dS' K^T (columns: tokens)
@@ -791,6 +792,18 @@ delta_adjoint_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int
     __syncthreads();   // the load warps' last one
     let_next_start();
     if (w.dinit) store_acc<N>(w.dinit + srow, D);
+    float f = 0.f;   // <dS, S> at the start
+    if (a.init) {
+        float S[NT][4];
+        load_acc<N>(a.init + srow, S);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) f = fmaf(D[n][r], S[n][r], f);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+    }
+    if (lane == 0) w.dot_ss[(b * (w.n64 + 1) * a.H + h) * (P / 16) + p0 / 16] = f;
 }
 
 // Rows of a head per CTA: all of them (half of 128), or fewer where the launch would leave SMs empty.
