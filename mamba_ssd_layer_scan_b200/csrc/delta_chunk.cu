@@ -209,15 +209,24 @@ delta_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, const int2 *t
 // Shared-memory stage of one chunk: K and Q of the group, then per head of the CTA its V (and dO,
 // for the backward), its triangles and its factors.  Rows are 16 bytes longer than their data.
 struct ChainStage {
-    int kpitch, vpitch, tri, vec, head, total;   // bytes; tri, vec: offsets in a head's part
+    int kpitch, vpitch, tri, vec, state, w, head, total;   // bytes; from tri on offsets in a head's part
     static constexpr int kTriPitch = C * 2 + 16;
     static constexpr int kTri = C * kTriPitch;
-    __host__ __device__ ChainStage(int rows, int N, int heads, bool bwd)
+    // bwd: with dO and Att's second part; adjoint: also the state behind a span, and W (in
+    // accumulator layout)
+    __host__ __device__ ChainStage(int rows, int N, int heads, bool bwd, bool adjoint = false)
         : kpitch(N * 2 + 16), vpitch(rows * 2 + 16), tri((bwd ? 2 : 1) * C * (rows * 2 + 16)),
-          vec(tri + (bwd ? 4 : 3) * kTri), head(vec + 512), total(2 * C * kpitch + heads * head)
+          vec(tri + (bwd ? 4 : 3) * kTri), state(vec + 512),
+          w(state + (adjoint ? rows * state_pitch(N) : 0)),
+          head(w + (adjoint ? rows * C * 4 : 0)), total(2 * C * kpitch + heads * head)
     {
     }
+    static __host__ __device__ constexpr int state_pitch(int N) { return N * 4 + 32; }
 };
+// The adjoint chain reads the states and W through its stage where a CTA has one warp of rows, bound by
+// what a chunk waits for (2 x 2048 tokens x 24 heads: 183 -> 162 us); with more rows the space is
+// worth more as a second CTA on the SM.
+__host__ __device__ constexpr bool adjoint_staged(int rows) { return rows == 16; }
 
 // The CTA's share of a launch: see delta_chain_kernel.
 struct ChainSlice {
@@ -594,7 +603,8 @@ delta_adjoint_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int
     wait_before();
     constexpr int NT = N / 8;
     const int P = a.P;
-    const ChainStage lay(rows, N, heads, true);
+    const bool staged = adjoint_staged(rows);
+    const ChainStage lay(rows, N, heads, true, staged);
     const ChainSlice slice(a, heads, rows, false);
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int hl = warp / (rows / 16), pl = warp % (rows / 16) * 16;
@@ -604,9 +614,23 @@ delta_adjoint_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int
     const uint32_t base = smem_u32(smem);
     if (hl >= heads) {   // the load warps
         for (int64_t c = nchunks - 1; c >= -1; --c) {
-            if (c >= 0)
-                load_stage<N, true>(a, lay, slice, items, w.dout, nchunks, nullptr, c,
-                                    base + ((nchunks - 1 - c) & 1) * lay.total);
+            const uint32_t to = base + ((nchunks - 1 - c) & 1) * lay.total;
+            if (c >= 0) load_stage<N, true>(a, lay, slice, items, w.dout, nchunks, nullptr, c, to);
+            if (c >= 0 && staged) {   // one head, 16 rows
+                const int i0 = tid % (kLoadWarps * 32);
+                const uint32_t head = to + 2 * C * lay.kpitch;
+                const int64_t item = (b * nchunks + c) * a.H + slice.h0;
+                const float *wf = w.wfrag + (item * (P / 16) + slice.pb / 16) * (16 * C);
+                for (int i = i0; i < 16 * C / 4; i += kLoadWarps * 32)
+                    cp16(head + lay.w + i * 16, wf + i * 4, true);
+                if (c % 2 == 1 || c == nchunks - 1) {
+                    const float *sn = w.states + (((b * (w.n64 + 1) + c / 2 + 1) * a.H + slice.h0) * P +
+                                                  slice.pb) * (int64_t)N;
+                    for (int i = i0; i < 16 * N / 4; i += kLoadWarps * 32)
+                        cp16(head + lay.state + i / (N / 4) * lay.state_pitch(N) + i % (N / 4) * 16,
+                             sn + i * 4, true);
+                }
+            }
             cp_commit();
             cp_wait<0>();
             __syncthreads();
@@ -627,24 +651,32 @@ delta_adjoint_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int
         const uint32_t ks = base + stage * lay.total, qs = ks + C * lay.kpitch;
         const uint32_t vs = qs + C * lay.kpitch + hl * lay.head;
         const uint32_t inv = vs + lay.tri, att = inv + 2 * ChainStage::kTri;
-        const float *vec = reinterpret_cast<const float *>(
-            smem + stage * lay.total + 2 * C * lay.kpitch + hl * lay.head + lay.vec);
+        const char *part = smem + stage * lay.total + 2 * C * lay.kpitch + hl * lay.head;
+        const float *vec = reinterpret_cast<const float *>(part + lay.vec);
         const int64_t item = (b * nchunks + c) * a.H + h;
         const int64_t tile = item * (P / 16) + p0 / 16;
         float4 wf[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-            wf[t] = reinterpret_cast<const float4 *>(w.wfrag + tile * (16 * C))[t * 32 + lane];
+            wf[t] = staged ? *reinterpret_cast<const float4 *>(part + lay.w + (t * 32 + lane) * 16)
+                           : reinterpret_cast<const float4 *>(w.wfrag + tile * (16 * C))[t * 32 + lane];
 
         if (c % 2 == 1 || c == nchunks - 1) {   // the end of a span of 64 tokens
             const int64_t span = (b * w.n64 + c / 2) * a.H + h;
+            // this lane's first row and the one 8 below
             const float *sn = w.states + ((b * (w.n64 + 1) + c / 2 + 1) * a.H + h) * P * N + pn;
+            int below = 8 * N;
+            if (staged) {
+                sn = reinterpret_cast<const float *>(part + lay.state + lane / 4 * lay.state_pitch(N)) +
+                     lane % 4 * 2;
+                below = 8 * lay.state_pitch(N) / 4;
+            }
             bf16 *ds = w.dstates + span * P * N + pn;
             float f = 0.f;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const float2 u = *reinterpret_cast<const float2 *>(sn + n * 8);
-                const float2 v = *reinterpret_cast<const float2 *>(sn + 8 * N + n * 8);
+                const float2 v = *reinterpret_cast<const float2 *>(sn + below + n * 8);
                 f = fmaf(D[n][0], u.x, fmaf(D[n][1], u.y, fmaf(D[n][2], v.x, fmaf(D[n][3], v.y, f))));
                 *reinterpret_cast<uint32_t *>(ds + n * 8) = pack_bf16x2(D[n][0], D[n][1]);
                 *reinterpret_cast<uint32_t *>(ds + 8 * N + n * 8) = pack_bf16x2(D[n][2], D[n][3]);
@@ -864,7 +896,7 @@ cudaError_t launch_delta_adjoint(const DeltaArgs &a, const DeltaBwd &w, const ch
     const int heads = 1, rows = chain_rows(a, a.batch);
     const unsigned grid = (unsigned)(a.batch * (a.H / heads) * (a.P / rows));
     const unsigned threads = (unsigned)((heads * rows / 16 + kLoadWarps) * 32);
-    const int smem = 2 * ChainStage(rows, a.N, heads, true).total;
+    const int smem = 2 * ChainStage(rows, a.N, heads, true, adjoint_staged(rows)).total;
     auto go = [&](auto kern) {
         return launch_after(kern, grid, threads, smem, st, a, w, items, nchunks, heads, rows);
     };
