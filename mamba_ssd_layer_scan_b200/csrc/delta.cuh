@@ -1,6 +1,9 @@
 // Internal interface of the gated delta rule's kernels (delta_*.cu).
 #pragma once
 
+#include <atomic>
+#include <mutex>
+
 #include "common.cuh"
 
 namespace ssd {
@@ -18,15 +21,38 @@ __device__ __forceinline__ void let_next_start()
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// Lets `kern` have `smem` bytes of dynamic shared memory on the current device; what it was given
+// before is remembered, the call takes a microsecond or two.
+inline cudaError_t allow_smem(const void *kern, size_t smem)
+{
+    if (smem <= 40 * 1024) return cudaSuccess;   // with the static part it fits anyway
+    constexpr int kKernels = 32, kDevices = 16;
+    static std::atomic<const void *> kernels[kKernels];
+    static std::atomic<int> given[kKernels][kDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::atomic<int> *mine = nullptr;
+    for (int i = 0; i < kKernels && dev < kDevices && !mine; ++i) {
+        const void *at = kernels[i].load();
+        if (!at && kernels[i].compare_exchange_strong(at, kern)) at = kern;
+        if (at == kern) mine = &given[i][dev];
+    }
+    if (mine && mine->load() >= (int)smem) return cudaSuccess;
+    static std::mutex one;   // no call may take back what another one has been given
+    const std::lock_guard<std::mutex> hold(one);
+    if (mine && mine->load() >= (int)smem) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && mine) mine->store((int)smem);
+    return e;
+}
+
 template <typename... Params, typename... Args>
 cudaError_t launch_after(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                          Args... args)
 {
-    if (smem > 40 * 1024) {   // with the static part this may pass 48 KB
-        const cudaError_t e =
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), smem);
+    if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;

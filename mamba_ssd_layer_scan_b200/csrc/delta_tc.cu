@@ -1028,8 +1028,7 @@ cudaError_t launch_delta_tc(const DeltaArgs &a, char *items, int64_t nchunks, co
     auto ctas = [&] { return nchunks * batch * a.G * ((hpg + run - 1) / run); };
     while (run > kPrepQuad && ctas() < 2 * 444) run = (run + 1) / 2;
     auto prep = [&](auto kern) {
-        cudaError_t e =
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrepSmem);
+        const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), kPrepSmem);
         if (e != cudaSuccess) return e;
         kern<<<(unsigned)ctas(), kPrepThreads, kPrepSmem, st>>>(a, items, nchunks, run, tab);
         return cudaGetLastError();

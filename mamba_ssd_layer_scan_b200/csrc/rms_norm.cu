@@ -14,6 +14,7 @@
 // A row of up to 32 vectors belongs to 8, 16 or 32 lanes of a warp, a longer one to a whole CTA;
 // the CTAs walk the rows with their slice of w in registers and the next rows on their way.
 #include <algorithm>
+#include <atomic>
 
 #include "api.cuh"
 #include "common.cuh"
@@ -534,11 +535,15 @@ rms_norm_dw_kernel(const float *part, float *dw, int n, int dim)
     if (lane == 0 && blockIdx.x * 32 + warp < dim) dw[blockIdx.x * 32 + warp] = t;
 }
 
+// Of the current device; asked once per device.
 int sm_count()
 {
+    static std::atomic<int> known[64];
     int dev = 0, n = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess)
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (cudaGetDevice(&dev) != cudaSuccess) return n;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed))) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 

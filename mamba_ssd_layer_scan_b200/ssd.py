@@ -564,13 +564,13 @@ def _on(t, name, shape, dtype, device):
 class _Call:
     """A call's device and stream (the device's current stream by default): allocates outputs and
     workspaces, and keeps their memory from being handed out again while that stream uses it."""
-    __slots__ = ("torch", "device", "handle", "other")
+    __slots__ = ("torch", "x", "device", "handle", "other")
 
     def __init__(self, x, stream):
         self.torch = torch = _torch()
         if not x.is_cuda:
             raise ValueError(f"tensors must be on a CUDA device, got {x.device}")
-        self.device = x.get_device()
+        self.x, self.device = x, x.get_device()
         self.handle = torch._C._cuda_getCurrentRawStream(self.device)
         self.other = None
         if stream is not None:
@@ -579,15 +579,22 @@ class _Call:
             if stream.cuda_stream != self.handle:
                 self.handle, self.other = stream.cuda_stream, stream
 
+    # empty_like and new_empty take half of torch.empty's time
+    def like(self, t, dtype=None):
+        """Uninitialised, with the shape of t, which is contiguous."""
+        return self._used(self.torch.empty_like(t, dtype=dtype))
+
     def empty(self, shape, dtype):
-        t = self.torch.empty(shape, dtype=dtype, device=self.device)
+        return self._used(self.x.new_empty(shape, dtype=dtype))
+
+    def _used(self, t):
         if self.other is not None:
             t.record_stream(self.other)
         return t
 
     def workspace(self, given, size):
         if given is None:
-            return self.empty(size, self.torch.uint8)
+            return self.empty((size,), self.torch.uint8)
         _on(given, "workspace", given.shape, self.torch.uint8, self.device)
         return given
 
@@ -675,12 +682,12 @@ def delta_rule_fwd(q, k, v, g, beta, scale=None, init_state=None, qk_l2norm: boo
                          ((init_state, "init_state"), (final_state, "final_state")))
     call, shape = _Call(v, stream), plan.shape
     if o is None:
-        o = call.empty(v.shape, v.dtype)
+        o = call.like(v)
     else:
         _on(o, "o", v.shape, v.dtype, call.device)
     if final_state is None and return_final_state:
-        final_state = call.empty((shape.batch, shape.nheads, shape.headdim, shape.dstate),
-                                 call.torch.float32)
+        final_state = call.like(init_state) if init_state is not None else call.empty(
+            (shape.batch, shape.nheads, shape.headdim, shape.dstate), call.torch.float32)
     workspace = call.workspace(workspace, plan.workspace_size("ssd_delta_rule_workspace_size"))
     call.run(lib().ssd_delta_rule_fwd, plan.ref, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
              _delta_options(scale, shape.dstate, qk_l2norm), _ptr(init_state), _ptr(o),
@@ -700,13 +707,13 @@ def delta_rule_varlen_fwd(q, k, v, g, beta, cu_seqlens, scale=None, init_states=
     _on(cu_seqlens, "cu_seqlens", (nseq + 1,), _torch().int32, v.get_device())
     call, shape = _Call(v, stream), plan.shape
     if o is None:
-        o = call.empty(v.shape, v.dtype)
+        o = call.like(v)
     else:
         _on(o, "o", v.shape, v.dtype, call.device)
     n = plan.workspace_size("ssd_delta_rule_varlen_workspace_size", nseq)
     if final_states is None and return_final_states:
-        final_states = call.empty((nseq, shape.nheads, shape.headdim, shape.dstate),
-                                  call.torch.float32)
+        final_states = call.like(init_states) if init_states is not None else call.empty(
+            (nseq, shape.nheads, shape.headdim, shape.dstate), call.torch.float32)
     workspace = call.workspace(workspace, n)
     call.run(lib().ssd_delta_rule_varlen_fwd, plan.ref, _ptr(q), _ptr(k), _ptr(v), _ptr(g),
              _ptr(beta), _delta_options(scale, shape.dstate, qk_l2norm), _ptr(cu_seqlens), nseq,
@@ -725,13 +732,11 @@ def delta_rule_bwd(q, k, v, g, beta, dout, scale=None, init_state=None, dfinal=N
     _on(dout, "dout", v.shape, v.dtype, v.get_device())
     call, shape = _Call(v, stream), plan.shape
     n = plan.workspace_size("ssd_delta_rule_bwd_workspace_size")
-    f32 = call.torch.float32
-    out = dict(dq=call.empty(q.shape, q.dtype), dk=call.empty(k.shape, k.dtype),
-               dv=call.empty(v.shape, v.dtype),
-               dg=None if g is None else call.empty(g.shape, f32),
-               dbeta=call.empty(beta.shape, f32),
-               dinit=call.empty((shape.batch, shape.nheads, shape.headdim, shape.dstate), f32)
-               if return_dinit else None)
+    out = dict(dq=call.like(q), dk=call.like(k), dv=call.like(v),
+               dg=None if g is None else call.like(g), dbeta=call.like(beta), dinit=None)
+    if return_dinit:
+        out["dinit"] = call.like(init_state) if init_state is not None else call.empty(
+            (shape.batch, shape.nheads, shape.headdim, shape.dstate), call.torch.float32)
     workspace = call.workspace(workspace, n)
     call.run(lib().ssd_delta_rule_bwd, plan.ref, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
              _delta_options(scale, shape.dstate, qk_l2norm), _ptr(init_state), _ptr(dout),
@@ -748,7 +753,7 @@ def delta_rule_update(state, q, k, v, g, beta, scale=None, qk_l2norm: bool = Fal
     plan = _delta_inputs(q, k, v, g, beta, None, ((state, "state"),), seq=False)
     call = _Call(v, stream)
     if o is None:
-        o = call.empty(v.shape, v.dtype)
+        o = call.like(v)
     else:
         _on(o, "o", v.shape, v.dtype, call.device)
     call.run(lib().ssd_delta_rule_update, plan.ref, _ptr(state), _ptr(q), _ptr(k), _ptr(v),
@@ -807,7 +812,7 @@ def rms_norm(x, weight, eps: float = 1e-5, residual=None, z=None, gate: str = "n
     torch = call.torch
     out_dtype = torch.float8_e4m3fn if quant_group else x.dtype
     if y is None:
-        y = call.empty(x.shape, out_dtype)
+        y = call.like(x, out_dtype)
     else:
         _on(y, "y", x.shape, out_dtype, call.device)
     if quant_group:
@@ -819,7 +824,7 @@ def rms_norm(x, weight, eps: float = 1e-5, residual=None, z=None, gate: str = "n
     elif scales is not None:
         raise ValueError("scales go with quant_group")
     if residual is not None and residual_out is None:
-        residual_out = call.empty(x.shape, x.dtype)
+        residual_out = call.like(x)
     call.run(lib().ssd_rms_norm, plan.ref, _ptr(x), _ptr(residual), _ptr(z), _ptr(weight), _ptr(y),
              _ptr(scales), _ptr(residual_out))
     out = [t for t in (y, scales, residual_out) if t is not None]
@@ -837,10 +842,9 @@ def rms_norm_bwd(x, weight, dy, eps: float = 1e-5, z=None, gate: str = "none", d
     if z is None and dz is not None:
         raise ValueError("dz goes with z")
     call = _Call(x, stream)
-    g = dict(dx=call.empty(x.shape, x.dtype) if dx is None else dx,
-             dweight=call.empty(weight.shape, call.torch.float32))
+    g = dict(dx=call.like(x) if dx is None else dx, dweight=call.like(weight))
     if z is not None:
-        g["dz"] = call.empty(x.shape, x.dtype) if dz is None else dz
+        g["dz"] = call.like(x) if dz is None else dz
     if plan.bwd_size == 0:   # the entry point says what it refuses
         lib().ssd_rms_norm_bwd_workspace_size(plan.ref)
         raise SSDError(SSD_ERR_INVALID_ARG, last_error())
