@@ -18,6 +18,7 @@
 
 #include "api.cuh"
 #include "common.cuh"
+#include "delta.cuh"
 #include "delta_mma.cuh"
 
 namespace ssd {
@@ -479,6 +480,7 @@ rms_norm_bwd_kernel(const NormArgs a)
         }
         w.next();
     }
+    let_next_start();
     // this CTA's partial weight gradient: one row of `dw_part`
     if constexpr (TPR == 0) {
 #pragma unroll
@@ -516,6 +518,7 @@ rms_norm_dw_kernel(const float *part, float *dw, int n, int dim)
     __shared__ float sums[32][33];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, col = blockIdx.x * 32 + lane;
     float s[4] = {};
+    wait_before();
     if (col < dim) {
         const float *p = part + col;
 #pragma unroll
@@ -594,8 +597,8 @@ cudaError_t launch(const NormArgs &a, bool bwd, int threads, float *dw, cudaStre
     cudaError_t e = launch_walk(rms_norm_bwd_kernel<T, VEC, NV, TPR, kMode>, a, per_cta, threads,
                                 smem, kBwdCtas, &ctas, st);
     if (e != cudaSuccess) return e;
-    rms_norm_dw_kernel<<<(a.dim + 31) / 32, 1024, 0, st>>>(a.dw_part, dw, (int)ctas, a.dim);
-    return cudaGetLastError();
+    return launch_after(rms_norm_dw_kernel, (a.dim + 31) / 32, 1024, 0, st, a.dw_part, dw, (int)ctas,
+                        a.dim);
 }
 
 // Threads of a CTA that takes one row of `vecs` vectors, NV per thread.
