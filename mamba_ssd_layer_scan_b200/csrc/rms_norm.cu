@@ -158,6 +158,14 @@ template <int VEC> __device__ __forceinline__ void times(float (&x)[VEC], const 
         for (int i = 0; i < VEC; i += 2)
             unpair(mul2(pair(x[i], x[i + 1]), pair(y[i], y[i + 1])), x[i], x[i + 1]);
 }
+template <int VEC> __device__ __forceinline__ void plus(float (&x)[VEC], const float (&y)[VEC])
+{
+    if constexpr (VEC == 1) x[0] += y[0];
+    else
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2)
+            unpair(add2(pair(x[i], x[i + 1]), pair(y[i], y[i + 1])), x[i], x[i + 1]);
+}
 template <int VEC> __device__ __forceinline__ void times(float (&x)[VEC], float f)
 {
     if constexpr (VEC == 1) x[0] *= f;
@@ -183,19 +191,24 @@ __device__ __forceinline__ float both(uint64_t p)
     return x + y;
 }
 
-// Reduces a (a sum) and b (a sum, or a maximum when kMax) over the threads of a row.  TPR: lanes
+// Reduces a (a sum) and b (a sum or a maximum, or not at all) over the threads of a row.  TPR: lanes
 // per row, 0 for the whole CTA; `buf` alternates between two halves from row to row, so that one
 // barrier per row is enough.
-template <int TPR, bool kMax>
+enum : int { kAlone, kSum, kMax };
+template <int kOther> __device__ __forceinline__ void reduce_step(float &a, float &b, int o)
+{
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    if constexpr (kOther != kAlone) {
+        const float other = __shfl_xor_sync(0xffffffffu, b, o);
+        b = kOther == kMax ? max_nan(b, other) : b + other;
+    }
+}
+template <int TPR, int kOther>
 __device__ __forceinline__ void reduce_row(float &a, float &b, float2 *red, int buf)
 {
     constexpr int W = TPR == 0 ? 32 : TPR;
 #pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        const float other = __shfl_xor_sync(0xffffffffu, b, o);
-        b = kMax ? max_nan(b, other) : b + other;
-    }
+    for (int o = W / 2; o > 0; o >>= 1) reduce_step<kOther>(a, b, o);
     if constexpr (TPR == 0) {   // every warp reduces the warps' results (at most 16) again
         const int warps = blockDim.x / 32, lane = threadIdx.x % 32;
         float2 *r = red + buf * (kMaxRowThreads / 32);
@@ -205,11 +218,7 @@ __device__ __forceinline__ void reduce_row(float &a, float &b, float2 *red, int 
         a = v.x;
         b = v.y;
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
-            a += __shfl_xor_sync(0xffffffffu, a, o);
-            const float other = __shfl_xor_sync(0xffffffffu, b, o);
-            b = kMax ? max_nan(b, other) : b + other;
-        }
+        for (int o = 8; o > 0; o >>= 1) reduce_step<kOther>(a, b, o);
     }
 }
 
@@ -336,8 +345,7 @@ rms_norm_kernel(const NormArgs a)
                 if constexpr (kMode != kPlain) w.get(1, j).get(other);
                 if constexpr (kMode == kResidual) {
                     Pack<T, VEC> sum;
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) h[j][i] += other[i];
+                    plus(h[j], other);
                     sum.set(h[j]);
                     sum.get(h[j]);
                     *reinterpret_cast<Pack<T, VEC> *>(static_cast<T *>(a.res_out) + w.at(j)) = sum;
@@ -357,7 +365,7 @@ rms_norm_kernel(const NormArgs a)
             }
         }
         float ss = both(sums);
-        reduce_row<TPR, true>(ss, top, red, buf);
+        reduce_row<TPR, kQuant == kPerRow ? kMax : kAlone>(ss, top, red, buf);
         const float r = rsqrtf(fmaf(ss, inv_dim, a.eps));
         float scale = max_nan(top * r * (1.f / kE4m3Max), kMinScale);
 #pragma unroll
@@ -448,7 +456,7 @@ rms_norm_bwd_kernel(const NormArgs a)
             add_products(dots, dy, x);
         }
         float ss = both(sums), dot = both(dots);
-        reduce_row<TPR, false>(ss, dot, red, buf);
+        reduce_row<TPR, kSum>(ss, dot, red, buf);
         const float r = rsqrtf(fmaf(ss, inv_dim, a.eps));
         const float c = dot * inv_dim * r * r * r;
 #pragma unroll
