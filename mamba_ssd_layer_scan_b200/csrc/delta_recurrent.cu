@@ -8,7 +8,8 @@
 // so that a token costs one reduction: the 2 kRows sums are folded over the lanes together, each
 // step halving the sums a lane carries (16 shuffles where kRows separate sums take 80).
 //
-// One token per sequence (decode) is HBM-bound on the float32 state, read and written once.  Many
+// One token per sequence (decode) is HBM-bound on the float32 state, read and written once (128
+// sequences x 80 heads of 64 x 128: 96-101 us, 6.7 TB/s; one sequence of 24 heads 4 us).  Many
 // tokens are bound by the latency of that reduction; the chunked kernels take over where they can.
 #include "delta.cuh"
 

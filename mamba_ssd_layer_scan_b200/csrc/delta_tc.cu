@@ -14,7 +14,10 @@
 // CTA multiply all 128 rows by each head's triangles and read their own result: 2 x 64 columns
 // cost the same as a block-diagonal product, and what is not finite in one head stays there.
 //
-// Bound: the chain of a chunk, three products deep, with the rows' splits between them.
+// Bound: the chain of a chunk, three products deep (500-700 cycles each) with the rows' splits and the
+// hand-overs between them, 5400 cycles: 2 x 4096 tokens x 32 heads of 128 take 180 us, 64 chunks of 2.8 us,
+// behind 50 us for the triangles; 16384 packed tokens x 80 heads of 64 250 us behind 150 us.  64 tokens
+// to a chunk: of 32 the same products would have half the columns, and the hand-overs twice their share.
 #include "delta.cuh"
 #include "delta_mma.cuh"
 
@@ -1027,6 +1030,7 @@ cudaError_t launch_delta_tc(const DeltaArgs &a, char *items, int64_t nchunks, co
     int run = hpg < 16 ? (int)hpg : 16;
     auto ctas = [&] { return nchunks * batch * a.G * ((hpg + run - 1) / run); };
     while (run > kPrepQuad && ctas() < 2 * 444) run = (run + 1) / 2;
+    if (ctas() > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     auto prep = [&](auto kern) {
         const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kern), kPrepSmem);
         if (e != cudaSuccess) return e;

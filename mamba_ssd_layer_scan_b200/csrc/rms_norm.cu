@@ -13,6 +13,8 @@
 // row's largest |h w| (forward, one scale per row) or with sum(dn w h) (backward) -- and written.
 // A row of up to 32 vectors belongs to 8, 16 or 32 lanes of a warp, a longer one to a whole CTA;
 // the CTAs walk the rows with their slice of w in registers and the next rows on their way.
+// Measured (bf16): 16384 x 2560 with a residual 60 us, 85 % of the copy bandwidth, its backward 68 + 4 us;
+// 8191 x 5120 gated, e4m3 by groups of 128, 50 us (64 %, issue slots); 98304 x 64 gated backward 17 + 4 us.
 #include <algorithm>
 #include <atomic>
 
