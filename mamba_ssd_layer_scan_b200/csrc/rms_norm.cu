@@ -63,6 +63,20 @@ template <> struct Pack<bf16, 1> {
     __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = __bfloat162float(v); }
     __device__ __forceinline__ void set(const float (&f)[1]) { v = __float2bfloat16_rn(f[0]); }
 };
+template <> struct __align__(8) Pack<float, 2> {
+    float2 v;
+    __device__ __forceinline__ void get(float (&f)[2]) const { f[0] = v.x; f[1] = v.y; }
+    __device__ __forceinline__ void set(const float (&f)[2]) { v = make_float2(f[0], f[1]); }
+};
+template <> struct __align__(4) Pack<bf16, 2> {
+    __nv_bfloat162 v;
+    __device__ __forceinline__ void get(float (&f)[2]) const
+    {
+        const float2 p = __bfloat1622float2(v);
+        f[0] = p.x; f[1] = p.y;
+    }
+    __device__ __forceinline__ void set(const float (&f)[2]) { v = __floats2bfloat162_rn(f[0], f[1]); }
+};
 template <> struct __align__(16) Pack<float, 4> {
     float4 v;
     __device__ __forceinline__ void get(float (&f)[4]) const
@@ -91,13 +105,6 @@ template <> struct __align__(16) Pack<bf16, 8> {
     }
 };
 
-template <typename T, int VEC>
-__device__ __forceinline__ void store(void *base, int64_t at, const float (&f)[VEC])
-{
-    Pack<T, VEC> p;
-    p.set(f);
-    *reinterpret_cast<Pack<T, VEC> *>(static_cast<T *>(base) + at) = p;
-}
 template <int VEC> __device__ __forceinline__ void load_w(const float *w, float (&f)[VEC])
 {
     if constexpr (VEC == 1) {
@@ -110,7 +117,10 @@ template <int VEC> __device__ __forceinline__ void load_w(const float *w, float 
         }
     }
 }
-
+template <typename T> __device__ __forceinline__ void store_one(void *base, int64_t at, float f)
+{
+    static_cast<T *>(base)[at] = from_f32<T>(f);
+}
 // Larger of two values, NaN if either is (so that a row with a NaN keeps it in its scale).
 __device__ __forceinline__ float max_nan(float a, float b)
 {
@@ -130,6 +140,8 @@ template <int VEC> __device__ __forceinline__ void store_e4m3(uint8_t *to, const
 {
     if constexpr (VEC == 1) {
         *to = (uint8_t)e4m3x2(f[0], 0.f);
+    } else if constexpr (VEC == 2) {
+        *reinterpret_cast<uint16_t *>(to) = e4m3x2(f[0], f[1]);
     } else if constexpr (VEC == 4) {
         *reinterpret_cast<uint32_t *>(to) =
             (uint32_t)e4m3x2(f[0], f[1]) | ((uint32_t)e4m3x2(f[2], f[3]) << 16);
@@ -225,19 +237,27 @@ __device__ __forceinline__ void reduce_row(float &a, float &b, float2 *red, int 
 }
 
 // How a CTA walks the rows, and this thread's share of a row: vectors j * threads + lane of VEC
-// elements, j < NV.  The operands' vectors of 16 bytes come some rows ahead through a ring in
-// shared memory (cp.async); a thread reads what it copied itself, so the ring needs no barrier.
+// elements, j < NV.  Rows of whole 16-byte vectors are taken in these; other rows in pairs, those that
+// start at an odd element one element earlier, so that a pair is aligned and only the row's ends are
+// taken one by one (3e7 bf16 values in rows of 7001 with a residual: 82 us, element by element 283, in
+// rows of 7000 52), the next row's in registers; element by element where a tensor starts between
+// pairs.  The operands' vectors of 16 bytes come some rows ahead through a ring in shared memory
+// (cp.async); a thread reads what it copied itself, so the ring needs no barrier.
 // With the next row in registers instead, 16384 x 2560 ran at 72 % (residual) and its backward
 // at 33 % of the copy bandwidth: too few warps fitted.
 __host__ __device__ constexpr int rows_ahead(int nv) { return nv == 1 ? 3 : nv == 2 ? 2 : 1; }
 template <typename T, int VEC, int NV, int TPR, int kOps> struct Walk {
     static constexpr bool kRing = sizeof(T) * VEC == 16;
     static constexpr int kAhead = rows_ahead(NV);
-    int tpr, lane, sub, dim;
+    int tpr, lane, sub, dim, shift;
     int64_t row, step, rows;
-    bool on[NV];
+    bool on[NV];     // some of vector j is in the row; all of it
+    bool full[NV];
     uint32_t slot;   // this thread's first slot in the ring
     int turn;
+    // without a ring: this row's vectors and, where a thread has few of them, the next row's
+    static constexpr bool kNext = !kRing && NV * VEC * sizeof(T) <= 32;
+    Pack<T, VEC> now[kOps][kRing ? 1 : NV], then[kOps][kNext ? NV : 1];
     const void *op[kOps];
 
     __device__ __forceinline__ Walk(const NormArgs &a, char *ring) : dim(a.dim), rows(a.rows), turn(0)
@@ -246,15 +266,22 @@ template <typename T, int VEC, int NV, int TPR, int kOps> struct Walk {
         lane = TPR == 0 ? threadIdx.x : threadIdx.x % tpr;
         sub = TPR == 0 ? 0 : threadIdx.x / tpr;
         const int per_cta = TPR == 0 ? 1 : kRowThreads / tpr;
-        step = (int64_t)gridDim.x * per_cta;
+        step = (int64_t)gridDim.x * per_cta;   // even where a thread has several rows of odd width
         row = (int64_t)blockIdx.x * per_cta + sub;
+        shift = VEC == 2 ? (int)(row & dim & 1) : 0;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) on[j] = (j * tpr + lane) * VEC < dim;
+        for (int j = 0; j < NV; ++j) {
+            full[j] = col(j) >= 0 && col(j) + VEC <= dim;
+            on[j] = VEC == 2 ? col(j) < dim : full[j];
+        }
         slot = smem_u32(ring) + threadIdx.x * 16;
     }
-    __device__ __forceinline__ int64_t at(int j) const
+    __device__ __forceinline__ int col(int j) const { return (j * tpr + lane) * VEC - shift; }
+    __device__ __forceinline__ int64_t at(int j) const { return row * dim + col(j); }
+    // of a vector at the row's end: whether element i is in the row
+    __device__ __forceinline__ bool in(int j, int i) const
     {
-        return row * dim + (j * tpr + lane) * VEC;
+        return (unsigned)(col(j) + i) < (unsigned)dim;
     }
     __device__ __forceinline__ uint32_t place(int o, int j) const
     {
@@ -274,14 +301,57 @@ template <typename T, int VEC, int NV, int TPR, int kOps> struct Walk {
             cp_commit();
         }
     }
+    // All vectors of a row, whatever is missing as zeros.  A pair across the row's end is read whole --
+    // its other half is the neighbouring row's -- but for the tensor's last element.
+    __device__ __forceinline__ void fetch(int64_t r, Pack<T, VEC> (*to)[NV]) const
+    {
+        const int64_t end = rows * dim;
+#pragma unroll
+        for (int o = 0; o < kOps; ++o)
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int64_t i = r * dim + col(j);
+                const T *from = static_cast<const T *>(op[o]) + i;
+                float f[VEC] = {};
+                Pack<T, VEC> p;
+                p.set(f);
+                if (r < rows && on[j]) {
+                    if (VEC == 1 || i + VEC <= end) {
+                        p = *reinterpret_cast<const Pack<T, VEC> *>(from);
+                    } else {
+                        f[0] = to_f32(*from);
+                        p.set(f);
+                    }
+                }
+                to[o][j] = p;
+            }
+    }
     __device__ __forceinline__ void start()
     {
-        for (int i = 0; i < kAhead; ++i) {
-            prefetch(i);
-            turn = turn + 1 == kAhead ? 0 : turn + 1;
+        if constexpr (kRing) {
+            for (int i = 0; i < kAhead; ++i) {
+                prefetch(i);
+                turn = turn + 1 == kAhead ? 0 : turn + 1;
+            }
+        } else if constexpr (kNext) {
+            fetch(row, then);
         }
     }
-    __device__ __forceinline__ void arrived() { if constexpr (kRing) cp_wait<kAhead - 1>(); }
+    // this row's vectors are there
+    __device__ __forceinline__ void arrived()
+    {
+        if constexpr (kRing) {
+            cp_wait<kAhead - 1>();
+        } else if constexpr (kNext) {
+#pragma unroll
+            for (int o = 0; o < kOps; ++o)
+#pragma unroll
+                for (int j = 0; j < NV; ++j) now[o][j] = then[o][j];
+            fetch(row + step, then);
+        } else {
+            fetch(row, now);
+        }
+    }
     // this thread's vector j of operand o
     __device__ __forceinline__ Pack<T, VEC> get(int o, int j) const
     {
@@ -292,21 +362,54 @@ template <typename T, int VEC, int NV, int TPR, int kOps> struct Walk {
                          : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(place(o, j)) : "memory");
             memcpy(&p, &v, 16);
         } else {
-            p = *reinterpret_cast<const Pack<T, VEC> *>(static_cast<const T *>(op[o]) + at(j));
+            p = now[o][j];
+            if (VEC == 2 && !full[j]) {
+                float f[VEC];
+                p.get(f);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) f[i] = in(j, i) ? f[i] : 0.f;
+                p.set(f);
+            }
         }
         return p;
     }
     // the next row; call it once this row's vectors have been used
     __device__ __forceinline__ void next()
     {
-        prefetch(kAhead);
-        turn = turn + 1 == kAhead ? 0 : turn + 1;
+        if constexpr (kRing) {
+            prefetch(kAhead);
+            turn = turn + 1 == kAhead ? 0 : turn + 1;
+        }
         row += step;
     }
     // the CTA's rows; the last ones may lie behind the end for some threads, which then only take
     // part in the reductions
     __device__ __forceinline__ bool more() const { return row - sub < rows; }
     __device__ __forceinline__ bool live() const { return row < rows; }
+    __device__ __forceinline__ void put(void *to, int j, const float (&f)[VEC]) const
+    {
+        if (VEC != 2 || full[j]) {
+            Pack<T, VEC> p;
+            p.set(f);
+            *reinterpret_cast<Pack<T, VEC> *>(static_cast<T *>(to) + at(j)) = p;
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (in(j, i)) store_one<T>(to, at(j) + i, f[i]);
+        }
+    }
+    // this thread's weights, zeros outside the row
+    __device__ __forceinline__ void weights(const float *w, float (&f)[NV][VEC]) const
+    {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) f[j][i] = VEC == 2 && in(j, i) ? w[col(j) + i] : 0.f;
+            if constexpr (VEC != 2) {
+                if (on[j]) load_w<VEC>(w + col(j), f[j]);
+            }
+        }
+    }
 };
 
 __host__ __device__ constexpr int norm_ops(int mode) { return mode == kPlain ? 1 : 2; }
@@ -325,12 +428,7 @@ rms_norm_kernel(const NormArgs a)
     if constexpr (kMode != kPlain) w.op[1] = kMode == kResidual ? a.residual : a.z;
     w.start();
     float wt[NV][VEC];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) wt[j][i] = 0.f;
-        if (w.on[j]) load_w<VEC>(a.w + (j * w.tpr + w.lane) * VEC, wt[j]);
-    }
+    w.weights(a.w, wt);
     for (int buf = 0; w.more(); buf ^= 1) {
         const bool live = w.live();
         float h[NV][VEC];
@@ -350,7 +448,7 @@ rms_norm_kernel(const NormArgs a)
                     plus(h[j], other);
                     sum.set(h[j]);
                     sum.get(h[j]);
-                    *reinterpret_cast<Pack<T, VEC> *>(static_cast<T *>(a.res_out) + w.at(j)) = sum;
+                    w.put(a.res_out, j, h[j]);
                 }
             }
             if constexpr (kMode == kPre || kMode == kPost) {
@@ -372,7 +470,7 @@ rms_norm_kernel(const NormArgs a)
         float scale = max_nan(top * r * (1.f / kE4m3Max), kMinScale);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int e = (j * w.tpr + w.lane) * VEC;
+            const int e = w.col(j);
             times(h[j], r);
             if constexpr (kQuant != kNoQuant) {
                 if constexpr (kQuant == kPerGroup) {   // 32, 64 or 128 elements: their lanes
@@ -391,7 +489,7 @@ rms_norm_kernel(const NormArgs a)
                 }
                 if (!live || !w.on[j]) continue;
                 if constexpr (kQuant == kPerRow) {
-                    if (e == 0) a.scales[w.row] = scale;
+                    if (j == 0 && w.lane == 0) a.scales[w.row] = scale;
                 } else if ((e & (a.quant - 1)) == 0) {
                     const int shift = 31 - __clz(a.quant);
                     a.scales[w.row * (dim >> shift) + (e >> shift)] = scale;
@@ -399,10 +497,17 @@ rms_norm_kernel(const NormArgs a)
                 float inv;   // of a scale between 1e-30 and 1e36: to 2^-23
                 asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
                 times(h[j], inv);
-                store_e4m3<VEC>(a.y8 + w.row * dim + e, h[j]);
+                uint8_t *to = a.y8 + w.at(j);
+                if (VEC != 2 || w.full[j]) {
+                    store_e4m3<VEC>(to, h[j]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i)
+                        if (w.in(j, i)) to[i] = (uint8_t)e4m3x2(h[j][i], 0.f);
+                }
             } else {
                 if (!live || !w.on[j]) continue;
-                store<T, VEC>(a.y, w.at(j), h[j]);
+                w.put(a.y, j, h[j]);
             }
         }
         w.next();
@@ -425,13 +530,8 @@ rms_norm_bwd_kernel(const NormArgs a)
     w.op[1] = a.dy;
     if constexpr (kMode != kPlain) w.op[2] = kGated ? a.z : a.dres;
     w.start();
-    float wt[NV][VEC], dw[NV][VEC];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) wt[j][i] = dw[j][i] = 0.f;
-        if (w.on[j]) load_w<VEC>(a.w + (j * w.tpr + w.lane) * VEC, wt[j]);
-    }
+    float wt[NV][VEC], dw[NV][VEC] = {};
+    w.weights(a.w, wt);
     for (int buf = 0; w.more(); buf ^= 1) {
         const bool live = w.live();
         Pack<T, VEC> xp[NV], yp[NV], tp[NV];
@@ -485,8 +585,8 @@ rms_norm_bwd_kernel(const NormArgs a)
                 if constexpr (kGated)
                     dz[i] = (kMode == kPre ? dh * x[i] : dy[i] * n * wt[j][i]) * slope;
             }
-            store<T, VEC>(a.dx, w.at(j), dx);
-            if constexpr (kGated) store<T, VEC>(a.dz, w.at(j), dz);
+            w.put(a.dx, j, dx);
+            if constexpr (kGated) w.put(a.dz, j, dz);
         }
         w.next();
     }
@@ -498,7 +598,8 @@ rms_norm_bwd_kernel(const NormArgs a)
             if (w.on[j])
 #pragma unroll
                 for (int i = 0; i < VEC; ++i)
-                    a.dw_part[(int64_t)blockIdx.x * dim + (j * w.tpr + w.lane) * VEC + i] = dw[j][i];
+                    if (VEC != 2 || w.in(j, i))
+                        a.dw_part[(int64_t)blockIdx.x * dim + w.col(j) + i] = dw[j][i];
     } else {   // the CTA's rows are added up in order, in the ring's place
         constexpr int kPer = kRowThreads / (TPR == 0 ? kRowThreads : TPR);
         float *part = reinterpret_cast<float *>(ring);   // kPer x dim
@@ -509,7 +610,7 @@ rms_norm_bwd_kernel(const NormArgs a)
             if (w.on[j])
 #pragma unroll
                 for (int i = 0; i < VEC; ++i)
-                    part[w.sub * dim + (j * w.tpr + w.lane) * VEC + i] = dw[j][i];
+                    if (VEC != 2 || w.in(j, i)) part[w.sub * dim + w.col(j) + i] = dw[j][i];
         __syncthreads();
         for (int e = threadIdx.x; e < dim; e += kRowThreads) {
             float s = 0.f;
@@ -579,6 +680,7 @@ cudaError_t launch_walk(K kern, const NormArgs &a, int per_cta, int threads, siz
         if (grid > sms * per_sm) grid = sms * (per_sm > 0 ? per_sm : 1);
     }
     if (grid > most) grid = most;
+    if (grid * per_cta < a.rows && grid > 1) grid &= ~int64_t(1);   // rows of odd width: see Walk
     if (ctas) *ctas = grid;
     kern<<<(unsigned)grid, threads, smem, st>>>(a);
     return cudaGetLastError();
@@ -596,7 +698,7 @@ cudaError_t launch(const NormArgs &a, bool bwd, int threads, float *dw, cudaStre
         };
         if (!a.quant) return go(rms_norm_kernel<T, VEC, NV, TPR, kMode, kNoQuant>);
         if (a.quant == a.dim) return go(rms_norm_kernel<T, VEC, NV, TPR, kMode, kPerRow>);
-        if constexpr (VEC > 1)   // a group of 32 or more divides dim: whole vectors
+        if constexpr (VEC > 2)   // a group of 32 or more divides dim: whole vectors
             return go(rms_norm_kernel<T, VEC, NV, TPR, kMode, kPerGroup>);
         return cudaErrorInvalidValue;
     }
@@ -616,10 +718,11 @@ int row_threads(int vecs, int nv) { return ((vecs + nv - 1) / nv + 31) / 32 * 32
 
 // Rows of up to 32 vectors on 8, 16 or 32 lanes (no barrier), longer ones on a CTA with as few
 // vectors per thread as its 512 threads allow.
-template <typename T, int VEC, int kMode>
-cudaError_t launch_sized(const NormArgs &a, bool bwd, float *dw, cudaStream_t st)
+template <typename T, int kMode>
+cudaError_t launch_vectors(const NormArgs &a, bool bwd, float *dw, cudaStream_t st)
 {
-    const int vecs = (a.dim + VEC - 1) / VEC;
+    constexpr int VEC = 16 / sizeof(T);
+    const int vecs = a.dim / VEC;
     if (vecs <= 8) return launch<T, VEC, 1, 8, kMode>(a, bwd, kRowThreads, dw, st);
     if (vecs <= 16) return launch<T, VEC, 1, 16, kMode>(a, bwd, kRowThreads, dw, st);
     if (vecs <= 32) return launch<T, VEC, 1, 32, kMode>(a, bwd, kRowThreads, dw, st);
@@ -629,31 +732,63 @@ cudaError_t launch_sized(const NormArgs &a, bool bwd, float *dw, cudaStream_t st
         return launch<T, VEC, 2, 0, kMode>(a, bwd, row_threads(vecs, 2), dw, st);
     if (vecs <= 4 * kMaxRowThreads)
         return launch<T, VEC, 4, 0, kMode>(a, bwd, row_threads(vecs, 4), dw, st);
-    if constexpr (VEC <= 4) {
-        if (vecs <= 8 * kMaxRowThreads)
-            return launch<T, VEC, 8, 0, kMode>(a, bwd, row_threads(vecs, 8), dw, st);
-    }
-    if constexpr (VEC == 1)
-        return launch<T, VEC, 32, 0, kMode>(a, bwd, row_threads(vecs, 32), dw, st);
+    if constexpr (VEC == 4)
+        return launch<T, VEC, 8, 0, kMode>(a, bwd, row_threads(vecs, 8), dw, st);
     return cudaErrorInvalidValue;   // not reached: kMaxDim elements fit
 }
 
-template <typename T, int VEC>
+// The same in pairs (a row of odd width may take one more): up to 128 of them on a warp.
+template <typename T, int kMode>
+cudaError_t launch_pairs(const NormArgs &a, bool bwd, float *dw, cudaStream_t st)
+{
+    const int pairs = a.dim / 2 + a.dim % 2;
+    if (pairs <= 8) return launch<T, 2, 1, 8, kMode>(a, bwd, kRowThreads, dw, st);
+    if (pairs <= 32) return launch<T, 2, 1, 32, kMode>(a, bwd, kRowThreads, dw, st);
+    if (pairs <= 64) return launch<T, 2, 2, 32, kMode>(a, bwd, kRowThreads, dw, st);
+    if (pairs <= 128) return launch<T, 2, 4, 32, kMode>(a, bwd, kRowThreads, dw, st);
+    if (pairs <= 2 * kMaxRowThreads)
+        return launch<T, 2, 2, 0, kMode>(a, bwd, row_threads(pairs, 2), dw, st);
+    if (pairs <= 4 * kMaxRowThreads)
+        return launch<T, 2, 4, 0, kMode>(a, bwd, row_threads(pairs, 4), dw, st);
+    if (pairs <= 8 * kMaxRowThreads)
+        return launch<T, 2, 8, 0, kMode>(a, bwd, row_threads(pairs, 8), dw, st);
+    return launch<T, 2, 16, 0, kMode>(a, bwd, row_threads(pairs, 16), dw, st);
+}
+
+template <typename T, int kMode>
+cudaError_t launch_elements(const NormArgs &a, bool bwd, float *dw, cudaStream_t st)
+{
+    if (a.dim <= 256) return launch<T, 1, 8, 32, kMode>(a, bwd, kRowThreads, dw, st);
+    if (a.dim <= 8 * kMaxRowThreads)
+        return launch<T, 1, 8, 0, kMode>(a, bwd, row_threads(a.dim, 8), dw, st);
+    return launch<T, 1, 32, 0, kMode>(a, bwd, row_threads(a.dim, 32), dw, st);
+}
+
+template <typename T, int kMode>
+cudaError_t launch_sized(const NormArgs &a, bool bwd, float *dw, cudaStream_t st)
+{
+    if (a.dim % (16 / sizeof(T)) == 0) return launch_vectors<T, kMode>(a, bwd, dw, st);
+    // (a null pointer is aligned)
+    const int n = 2 * sizeof(T);
+    const bool pairs = api_aligned(a.x, n) && api_aligned(a.residual, n) && api_aligned(a.z, n) &&
+                       api_aligned(a.dy, n) && api_aligned(a.dres, n) && api_aligned(a.dx, n) &&
+                       api_aligned(a.dz, n) && api_aligned(a.res_out, n) &&
+                       api_aligned(a.y, bwd || !a.quant ? n : 2);
+    return pairs ? launch_pairs<T, kMode>(a, bwd, dw, st) : launch_elements<T, kMode>(a, bwd, dw, st);
+}
+
+template <typename T>
 cudaError_t launch_mode(const NormArgs &a, bool bwd, float *dw, cudaStream_t st)
 {
-    if (a.gate == SSD_GATE_PRE) return launch_sized<T, VEC, kPre>(a, bwd, dw, st);
-    if (a.gate == SSD_GATE_POST) return launch_sized<T, VEC, kPost>(a, bwd, dw, st);
-    if (bwd ? a.dres : a.residual) return launch_sized<T, VEC, kResidual>(a, bwd, dw, st);
-    return launch_sized<T, VEC, kPlain>(a, bwd, dw, st);
+    if (a.gate == SSD_GATE_PRE) return launch_sized<T, kPre>(a, bwd, dw, st);
+    if (a.gate == SSD_GATE_POST) return launch_sized<T, kPost>(a, bwd, dw, st);
+    if (bwd ? a.dres : a.residual) return launch_sized<T, kResidual>(a, bwd, dw, st);
+    return launch_sized<T, kPlain>(a, bwd, dw, st);
 }
 
 cudaError_t launch_norm(const NormArgs &a, bool is_bf16, bool bwd, float *dw, cudaStream_t st)
 {
-    if (is_bf16)
-        return a.dim % 8 ? launch_mode<bf16, 1>(a, bwd, dw, st)
-                         : launch_mode<bf16, 8>(a, bwd, dw, st);
-    return a.dim % 4 ? launch_mode<float, 1>(a, bwd, dw, st)
-                     : launch_mode<float, 4>(a, bwd, dw, st);
+    return is_bf16 ? launch_mode<bf16>(a, bwd, dw, st) : launch_mode<float>(a, bwd, dw, st);
 }
 
 ssd_status check_norm(const ssd_norm_desc *d)

@@ -212,3 +212,59 @@ def test_captured_calls_see_new_inputs(cuda_device):
         torch.cuda.synchronize()
         assert all(torch.equal(a.float(), b.float()) for a, b in zip(out, want))
         assert all(torch.equal(grads[k], wgrads[k]) for k in grads)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("dim", [1, 2, 15, 17, 63, 65, 130, 257, 513, 1537, 2049, 4097, 8191, 16383])
+@pytest.mark.parametrize("offset", [0, 1, 2])
+def test_rows_of_any_width_at_any_start(cuda_device, dim, dtype, offset):
+    """Rows that are not whole 16-byte vectors, starting at any element, next to others: the values, and
+    nothing written beside them (also in place)."""
+    rows = 45
+    if dim % (8 if dtype == torch.bfloat16 else 4) == 0:
+        pytest.skip("whole vectors")
+    d = _draw(rows, dim, dtype, seed=dim + offset)
+
+    def placed(t, fill=None):
+        buf = torch.full((t.numel() + 16,), 7.0, dtype=t.dtype, device=cuda_device)
+        view = buf[offset:offset + t.numel()].view(t.shape)
+        if fill is None:
+            view.copy_(t)
+        return buf, view
+
+    def clean(buf, n):
+        return bool((buf[:offset].float() == 7).all() and (buf[offset + n:].float() == 7).all())
+
+    n = rows * dim
+    c = {k: placed(d[k])[1] for k in ("x", "residual", "z", "dy")}
+    w = d["w"].to(cuda_device)
+    xb, x = placed(d["x"])
+    rb, r = placed(d["residual"])
+    y_ref, h_ref = ref.rms_norm(d["x"], d["w"], EPS, residual=d["residual"])
+    ssd.rms_norm(x, w, eps=EPS, residual=r, y=x, residual_out=r)
+    tol = STEP[dtype] + F32
+    assert ((x.double().cpu() - y_ref).abs() <= tol * y_ref.abs() + F32 * y_ref.abs().max()).all()
+    assert torch.equal(r.cpu(), h_ref) and clean(xb, n) and clean(rb, n)
+    y8b, y8 = placed(torch.zeros(rows, dim).to(torch.float8_e4m3fn))
+    y8, scales = ssd.rms_norm(c["x"], w, eps=EPS, z=c["z"], gate="pre", quant_group=dim, y=y8)
+    y_ref, _ = ref.rms_norm(d["x"], d["w"], EPS, z=d["z"], gate="pre")
+    got = y8.float().double().cpu() * scales.double().cpu()
+    s_ref = (y_ref.abs().amax(-1, keepdim=True) / 448).clamp_min(1e-30)
+    assert ((got - y_ref).abs() <= (2.0 ** -4 + 4 * F32) * y_ref.abs() + (2.0 ** -10 + F32) * s_ref).all()
+    assert clean(y8b, n)
+    dx, dw, dz = _grads(d, EPS, "post", False)
+    gb, g = placed(d["dy"])
+    zb, gz = placed(d["z"])
+    out = ssd.rms_norm_bwd(c["x"], w, g, eps=EPS, z=c["z"], gate="post", dx=g, dz=gz)
+    # dx is the difference of r dn w and h r^3 sum(dn w h) / dim, neither longer than r |dn w| (for the
+    # second: |h|^2 r^2 / dim <= 1); dz is dy n w times silu's slope, itself a sum of two terms below 1.1.
+    # Both are held to float32's error in the terms, and to the storage type's in the result.
+    x64, w64, dy64, z64 = (d[k].double() for k in ("x", "w", "dy", "z"))
+    r = torch.rsqrt((x64 * x64).mean(-1, keepdim=True) + EPS)
+    terms = (r * (dy64 * ref.silu(z64) * w64).norm(dim=-1, keepdim=True),
+             (dy64 * x64 * r * w64).norm(dim=-1, keepdim=True))
+    for got, want, size in ((out["dx"], dx, terms[0]), (out["dz"], dz, terms[1])):
+        err = (got.double().cpu() - want).norm(dim=-1, keepdim=True)
+        assert (err <= (STEP[dtype] + 2 * F32) * want.norm(dim=-1, keepdim=True) + 4 * F32 * size).all()
+    assert ref.rel(out["dweight"], dw) <= 256 * 2.0 ** -24 * 8
+    assert clean(gb, n) and clean(zb, n)
