@@ -289,15 +289,10 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
 
 // A warp per (token, group): sums the runs in order and undoes the norms.
 template <int N>
-__global__ void __launch_bounds__(256)
-delta_qk_kernel(const DeltaArgs a, const DeltaBwd w, int64_t rows)
+__device__ __forceinline__ void qk_row(const DeltaArgs &a, const DeltaBwd &w, int64_t row)
 {
     constexpr int V = N / 32;
-    let_next_start();
-    wait_before();
-    const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;   // (b, t, g)
     const int lane = threadIdx.x % 32;
-    if (row >= rows) return;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
         const float *part = (which ? w.dk_part : w.dq_part) + row * w.runs * N + lane * V;
@@ -330,13 +325,10 @@ delta_qk_kernel(const DeltaArgs a, const DeltaBwd w, int64_t rows)
 }
 
 // A warp per (span, head): dbeta, and dg by a reverse running sum; lane has tokens 2 l, 2 l + 1.
-__global__ void __launch_bounds__(256)
-delta_gate_kernel(const DeltaArgs a, const DeltaBwd w, int64_t nchunks, int64_t spans)
+__device__ __forceinline__ void gate_span(const DeltaArgs &a, const DeltaBwd &w, int64_t nchunks,
+                                          int64_t item)
 {
-    wait_before();
-    const int64_t item = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;   // (b, span, h)
     const int lane = threadIdx.x % 32;
-    if (item >= spans) return;
     const int h = (int)(item % a.H);
     const int64_t span = item / a.H % w.n64, b = item / a.H / w.n64;
     const int tiles = a.P / 16;
@@ -389,6 +381,17 @@ delta_gate_kernel(const DeltaArgs a, const DeltaBwd w, int64_t nchunks, int64_t 
     }
 }
 
+// The last kernel: a warp per item, (b, t, g) rows of dq and dk first, then (b, span, h).
+template <int N>
+__global__ void __launch_bounds__(256)
+delta_finish_kernel(const DeltaArgs a, const DeltaBwd w, int64_t nchunks, int64_t rows, int64_t spans)
+{
+    wait_before();
+    const int64_t item = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+    if (item < rows) qk_row<N>(a, w, item);
+    else if (item < rows + spans) gate_span(a, w, nchunks, item - rows);
+}
+
 }  // namespace
 
 cudaError_t launch_delta_grads(const DeltaArgs &a, const DeltaBwd &w, int64_t nchunks,
@@ -401,11 +404,8 @@ cudaError_t launch_delta_grads(const DeltaArgs &a, const DeltaBwd &w, int64_t nc
                      smem, st, a, w);
     if (e != cudaSuccess) return e;
     const int64_t rows = a.batch * a.L * a.G, spans = a.batch * w.n64 * a.H;
-    e = launch_after(a.N == 128 ? delta_qk_kernel<128> : delta_qk_kernel<64>,
-                     (unsigned)((rows + 7) / 8), 256, 0, st, a, w, rows);
-    if (e != cudaSuccess) return e;
-    return launch_after(delta_gate_kernel, (unsigned)((spans + 7) / 8), 256, 0, st, a, w, nchunks,
-                        spans);
+    return launch_after(a.N == 128 ? delta_finish_kernel<128> : delta_finish_kernel<64>,
+                        (unsigned)((rows + spans + 7) / 8), 256, 0, st, a, w, nchunks, rows, spans);
 }
 
 }  // namespace ssd
