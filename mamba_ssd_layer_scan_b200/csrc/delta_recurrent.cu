@@ -2,7 +2,8 @@
 //
 //     S <- exp(g) S,   u = beta (v - S k),   S <- S + u k^T,   o = scale S q
 //
-// The rows p of a state are independent, so a warp takes kRows of them through all tokens of a
+// The rows p of a state are independent, so a warp takes kRows of them (8; 4 or 2 where the launch would
+// leave SM quarters without a warp) through all tokens of a
 // sequence with the rows in registers (lane l holds elements l V .. l V + V - 1 of each).  Both dot
 // products of a token are taken of the state as it stands -- S_new q = exp(g) S q + u (k . q) --
 // so that a token costs one reduction: the 2 kRows sums are folded over the lanes together, each
@@ -16,7 +17,6 @@
 namespace ssd {
 namespace {
 
-constexpr int kRows = 8;    // state rows per warp
 constexpr int kWarps = 4;
 
 template <int V> __device__ __forceinline__ void load_state(const float *p, float (&r)[V])
@@ -56,7 +56,7 @@ __device__ __forceinline__ float warp_sum(float v)
 }
 
 // grid.x = ceil(P / (kRows kWarps)) * H * sequences
-template <typename T, int V>
+template <typename T, int V, int kRows>
 __global__ void __launch_bounds__(kWarps * 32)
 delta_recurrent_kernel(const DeltaArgs a, const int *status)
 {
@@ -89,7 +89,9 @@ delta_recurrent_kernel(const DeltaArgs a, const int *status)
     }
 
     const int g = h / (a.H / a.G);
-    const int row = (lane >> 1) & (kRows - 1);   // the row whose sums this lane ends up with
+    // the row whose sums this lane ends up with, the same as kSame - 1 neighbours
+    constexpr int kSame = 16 / kRows;
+    const int row = lane / kSame % kRows;
     const bool on = row < rows;
     const T *kp = static_cast<const T *>(a.k) + (t * a.G + g) * N + lane * V;
     const T *qp = static_cast<const T *>(a.q) + (t * a.G + g) * N + lane * V;
@@ -130,7 +132,7 @@ delta_recurrent_kernel(const DeltaArgs a, const int *status)
         const float v = to_f32(vn), beta = bn, decay = gp ? expf(gn) : 1.f;
         if (t + 1 < end) fetch();
 
-        // lane: sum index bit 4 (0: S k, 1: S q), row bits 3..1; bit 0 a duplicate
+        // lane: sum index bit 4 (0: S k, 1: S q), then the row's bits; the lowest are duplicates
         float c[2 * kRows];
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
@@ -152,7 +154,9 @@ delta_recurrent_kernel(const DeltaArgs a, const int *status)
                 c[i] = mine + __shfl_xor_sync(0xffffffffu, other, o);
             }
         }
-        float dot = c[0] + __shfl_xor_sync(0xffffffffu, c[0], 1);
+        float dot = c[0];
+#pragma unroll
+        for (int o = kSame / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
         kq = warp_sum(kq);
         float rk = 1.f, rq = a.scale;
         if (a.l2norm) {
@@ -163,11 +167,11 @@ delta_recurrent_kernel(const DeltaArgs a, const int *status)
         dot *= decay;
         float u = beta * (v - dot * rk) * rk;
         const float ku = __shfl_xor_sync(0xffffffffu, u, 16);
-        if (lane >= 16 && on && !(lane & 1)) *op = from_f32<T>(rq * fmaf(ku, kq, dot));
+        if (lane >= 16 && on && lane % kSame == 0) *op = from_f32<T>(rq * fmaf(ku, kq, dot));
         op += (int64_t)a.H * a.P;
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-            const float ur = __shfl_sync(0xffffffffu, u, 2 * r);
+            const float ur = __shfl_sync(0xffffffffu, u, kSame * r);
 #pragma unroll
             for (int i = 0; i < V; ++i) s[r][i] = fmaf(decay, s[r][i], ur * k[i]);
         }
@@ -179,19 +183,34 @@ delta_recurrent_kernel(const DeltaArgs a, const int *status)
     }
 }
 
+template <typename T, int V>
+cudaError_t launch_sized(const DeltaArgs &a, const int *status, cudaStream_t st)
+{
+    const int64_t states = (a.cu ? a.nseq : a.batch) * a.H;
+    auto go = [&](auto kern, int rows) {
+        const int pblocks = (a.P + rows * kWarps - 1) / (rows * kWarps);
+        kern<<<(unsigned)(states * pblocks), kWarps * 32, 0, st>>>(a, status);
+        return cudaGetLastError();
+    };
+    // fewer rows to a warp shorten its token while the launch has few warps for an SM quarter (float32,
+    // heads of 64 x 128, us with 8, 4 and 2 rows: 1500 tokens, 8 heads 785, 606, 556; 500 tokens, 37 heads
+    // 264, 204, 240; 74 heads 264, 253, 324; 148 heads 344, 367, 591; one token, 128 x 80 heads 100, 101, 152)
+    constexpr int64_t kQuarters = 148 * 4;
+    if (states * a.P <= 2 * kQuarters) return go(delta_recurrent_kernel<T, V, 2>, 2);
+    if (states * a.P <= 8 * kQuarters) return go(delta_recurrent_kernel<T, V, 4>, 4);
+    return go(delta_recurrent_kernel<T, V, 8>, 8);
+}
+
 template <typename T>
 cudaError_t launch_typed(const DeltaArgs &a, const int *status, cudaStream_t st)
 {
-    const int pblocks = (a.P + kRows * kWarps - 1) / (kRows * kWarps);
-    const unsigned grid = (unsigned)((a.cu ? a.nseq : a.batch) * a.H * pblocks);
     switch (a.N) {
-    case 32: delta_recurrent_kernel<T, 1><<<grid, kWarps * 32, 0, st>>>(a, status); break;
-    case 64: delta_recurrent_kernel<T, 2><<<grid, kWarps * 32, 0, st>>>(a, status); break;
-    case 128: delta_recurrent_kernel<T, 4><<<grid, kWarps * 32, 0, st>>>(a, status); break;
-    case 256: delta_recurrent_kernel<T, 8><<<grid, kWarps * 32, 0, st>>>(a, status); break;
+    case 32: return launch_sized<T, 1>(a, status, st);
+    case 64: return launch_sized<T, 2>(a, status, st);
+    case 128: return launch_sized<T, 4>(a, status, st);
+    case 256: return launch_sized<T, 8>(a, status, st);
     default: return cudaErrorInvalidValue;
     }
-    return cudaGetLastError();
 }
 
 }  // namespace
