@@ -248,7 +248,7 @@ __device__ __forceinline__ void reduce_row(float &a, float &b, float2 *red, int 
 __host__ __device__ constexpr int rows_ahead(int nv) { return nv == 1 ? 3 : nv == 2 ? 2 : 1; }
 template <typename T, int VEC, int NV, int TPR, int kOps> struct Walk {
     static constexpr bool kRing = sizeof(T) * VEC == 16;
-    static constexpr int kAhead = rows_ahead(NV);
+    [[maybe_unused]] static constexpr int kAhead = rows_ahead(NV);
     int tpr, lane, sub, dim, shift;
     int64_t row, step, rows;
     bool on[NV];     // some of vector j is in the row; all of it
