@@ -248,7 +248,6 @@ __device__ __forceinline__ void reduce_row(float &a, float &b, float2 *red, int 
 __host__ __device__ constexpr int rows_ahead(int nv) { return nv == 1 ? 3 : nv == 2 ? 2 : 1; }
 template <typename T, int VEC, int NV, int TPR, int kOps> struct Walk {
     static constexpr bool kRing = sizeof(T) * VEC == 16;
-    [[maybe_unused]] static constexpr int kAhead = rows_ahead(NV);
     int tpr, lane, sub, dim, shift;
     int64_t row, step, rows;
     bool on[NV];     // some of vector j is in the row; all of it
@@ -329,9 +328,9 @@ template <typename T, int VEC, int NV, int TPR, int kOps> struct Walk {
     __device__ __forceinline__ void start()
     {
         if constexpr (kRing) {
-            for (int i = 0; i < kAhead; ++i) {
+            for (int i = 0; i < rows_ahead(NV); ++i) {
                 prefetch(i);
-                turn = turn + 1 == kAhead ? 0 : turn + 1;
+                turn = turn + 1 == rows_ahead(NV) ? 0 : turn + 1;
             }
         } else if constexpr (kNext) {
             fetch(row, then);
@@ -341,7 +340,7 @@ template <typename T, int VEC, int NV, int TPR, int kOps> struct Walk {
     __device__ __forceinline__ void arrived()
     {
         if constexpr (kRing) {
-            cp_wait<kAhead - 1>();
+            cp_wait<rows_ahead(NV) - 1>();
         } else if constexpr (kNext) {
 #pragma unroll
             for (int o = 0; o < kOps; ++o)
@@ -377,8 +376,8 @@ template <typename T, int VEC, int NV, int TPR, int kOps> struct Walk {
     __device__ __forceinline__ void next()
     {
         if constexpr (kRing) {
-            prefetch(kAhead);
-            turn = turn + 1 == kAhead ? 0 : turn + 1;
+            prefetch(rows_ahead(NV));
+            turn = turn + 1 == rows_ahead(NV) ? 0 : turn + 1;
         }
         row += step;
     }
