@@ -21,6 +21,10 @@
 // enter as two bf16 parts each (2^-16), so that the state is carried to float32's usual accuracy:
 // 146 of the 184 matrix instructions per warp and chunk (P = 64, N = 128).  The output, rounded to
 // bf16 at once, takes the first parts only.
+// The backward's dg is a small difference of these products: what two parts leave of the values that
+// are written, of dS in dS K^T and of W in Att W came to 1e-5 and more of dg for one call in fifty of a
+// few tokens and heads (2.7e-5 at worst of 1800 such calls).  There these take three parts, and that is
+// 6e-6 at worst; 44 and 32 matrix instructions more in the two chains, 413 -> 451 us at 2 x 2048 x 24 heads.
 //
 // Bound: with many heads the rate of the warp-level matrix instructions (one m16n8k16 in 8 cycles per
 // SM quarter), where the tcgen05 form takes over; with few, where a warp has its SM quarter to itself,
@@ -502,9 +506,12 @@ delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64
         }
         // O += Att W
         {
-            uint32_t hi[2][4], lo[2][4];
-            split_a(W[0], W[1], hi[0], lo[0]);
-            split_a(W[2], W[3], hi[1], lo[1]);
+            uint32_t hi[2][4], lo[2][4], rest[2][4];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if constexpr (kBwd) split_a(W[2 * s], W[2 * s + 1], hi[s], lo[s], rest[s]);
+                else round_a(W[2 * s], W[2 * s + 1], hi[s]);
+            }
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -520,6 +527,8 @@ delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64
                         if (kBwd) {
                             mma_16816(O[2 * n + m], lo[s], fb[2 * m], fb[2 * m + 1]);
                             mma_16816(O[2 * n + m], hi[s], fl[2 * m], fl[2 * m + 1]);
+                            mma_16816(O[2 * n + m], rest[s], fb[2 * m], fb[2 * m + 1]);
+                            mma_16816(O[2 * n + m], lo[s], fl[2 * m], fl[2 * m + 1]);
                         }
                     }
                 }
@@ -565,8 +574,9 @@ delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            uint32_t hi[4], lo[4];
-            split_a(W[2 * s], W[2 * s + 1], hi, lo);
+            uint32_t hi[4], lo[4], rest[4];
+            if constexpr (kBwd) split_a(W[2 * s], W[2 * s + 1], hi, lo, rest);
+            else split_a(W[2 * s], W[2 * s + 1], hi, lo);
 #pragma unroll
             for (int n = 0; n < NT / 2; ++n) {
                 uint32_t fb[4];
@@ -575,6 +585,10 @@ delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64
                 mma_16816(S[2 * n + 1], hi, fb[2], fb[3]);
                 mma_16816(S[2 * n], lo, fb[0], fb[1]);
                 mma_16816(S[2 * n + 1], lo, fb[2], fb[3]);
+                if constexpr (kBwd) {
+                    mma_16816(S[2 * n], rest, fb[0], fb[1]);
+                    mma_16816(S[2 * n + 1], rest, fb[2], fb[3]);
+                }
             }
         }
         if constexpr (!kBwd)
@@ -695,8 +709,8 @@ delta_adjoint_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int
         float Y[4][4] = {};
 #pragma unroll
         for (int s = 0; s < N / 16; ++s) {
-            uint32_t hi[4], lo[4], fb[4];
-            split_a(D[2 * s], D[2 * s + 1], hi, lo);
+            uint32_t hi[4], lo[4], rest[4], fb[4];
+            split_a(D[2 * s], D[2 * s + 1], hi, lo, rest);
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 ldsm4(fb, ks + (n * 16 + row_nn) * lay.kpitch + s * 32 + col_nn);
@@ -704,6 +718,8 @@ delta_adjoint_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int
                 mma_16816(Y[2 * n + 1], hi, fb[2], fb[3]);
                 mma_16816(Y[2 * n], lo, fb[0], fb[1]);
                 mma_16816(Y[2 * n + 1], lo, fb[2], fb[3]);
+                mma_16816(Y[2 * n], rest, fb[0], fb[1]);
+                mma_16816(Y[2 * n + 1], rest, fb[2], fb[3]);
             }
         }
 #pragma unroll

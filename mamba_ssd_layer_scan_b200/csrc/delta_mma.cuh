@@ -53,6 +53,20 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     split2(sm100::pair(x, y), hi, lo);
 }
 
+// Three parts: hi + mid + lo is x to 2^-24 of it.
+__device__ __forceinline__ void split3(uint64_t xy, uint32_t &hi, uint32_t &mid, uint32_t &lo)
+{
+    const uint64_t minus = sm100::pair(-1.f, -1.f);
+    float x, y;
+    sm100::unpair(xy, x, y);
+    hi = sm100::pack_bf16x2(x, y);
+    xy = sm100::fma2(sm100::pair(bf16_lo(hi), bf16_hi(hi)), minus, xy);
+    sm100::unpair(xy, x, y);
+    mid = sm100::pack_bf16x2(x, y);
+    sm100::unpair(sm100::fma2(sm100::pair(bf16_lo(mid), bf16_hi(mid)), minus, xy), x, y);
+    lo = sm100::pack_bf16x2(x, y);
+}
+
 // The two parts one at a time.
 __device__ __forceinline__ uint32_t round2(uint64_t xy)
 {
@@ -75,6 +89,14 @@ __device__ __forceinline__ void split_a(const float (&t0)[4], const float (&t1)[
     split2(t0[2], t0[3], hi[1], lo[1]);
     split2(t1[0], t1[1], hi[2], lo[2]);
     split2(t1[2], t1[3], hi[3], lo[3]);
+}
+__device__ __forceinline__ void split_a(const float (&t0)[4], const float (&t1)[4],
+                                        uint32_t (&hi)[4], uint32_t (&mid)[4], uint32_t (&lo)[4])
+{
+    split3(sm100::pair(t0[0], t0[1]), hi[0], mid[0], lo[0]);
+    split3(sm100::pair(t0[2], t0[3]), hi[1], mid[1], lo[1]);
+    split3(sm100::pair(t1[0], t1[1]), hi[2], mid[2], lo[2]);
+    split3(sm100::pair(t1[2], t1[3]), hi[3], mid[3], lo[3]);
 }
 __device__ __forceinline__ void round_a(const float (&t0)[4], const float (&t1)[4],
                                         uint32_t (&hi)[4])
