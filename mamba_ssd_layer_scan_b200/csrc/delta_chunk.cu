@@ -22,7 +22,7 @@
 // 146 of the 184 matrix instructions per warp and chunk (P = 64, N = 128).  The output, rounded to
 // bf16 at once, takes the first parts only.
 // The backward's dg is a small difference of these products: what two parts leave of the values that
-// are written, of dS in dS K^T and of W in Att W came to 1e-5 and more of dg for one call in fifty of a
+// are written, of dS in dS K^T and of W in Att W came to 1e-5 and more of dg for one call in eighty of a
 // few tokens and heads (2.7e-5 at worst of 1800 such calls).  There these take three parts, and that is
 // 6e-6 at worst; 44 and 32 matrix instructions more in the two chains, 413 -> 451 us at 2 x 2048 x 24 heads.
 //

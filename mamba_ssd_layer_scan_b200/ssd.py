@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import re
 from typing import Optional
@@ -658,10 +659,14 @@ def _delta_inputs(q, k, v, g, beta, state_rows, states, seq=True):
     return _delta_plan(b, L, H, P, N, G, code)
 
 
-@functools.lru_cache(maxsize=64)
 def _delta_options(scale, dstate, qk_l2norm):
-    return ctypes.byref(DeltaOptions(dstate ** -0.5 if scale is None else scale,
-                                     1 if qk_l2norm else 0))
+    # the values: a tensor is hashed by identity, and its value may change
+    return _kept_options(dstate ** -0.5 if scale is None else float(scale), 1 if qk_l2norm else 0)
+
+
+@functools.lru_cache(maxsize=64)
+def _kept_options(scale, qk_l2norm):
+    return ctypes.byref(DeltaOptions(scale, qk_l2norm))
 
 
 def delta_rule_workspace_size(shape: Shape) -> int:
@@ -780,6 +785,8 @@ def _norm_inputs(x, weight, eps, z, gate, quant_group, others) -> _NormPlan:
         raise ValueError("z goes with a gate, and a gate with z")
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError(f"x must be (..., dim), got {tuple(x.shape)}")
+    # the values are kept: a tensor is hashed by identity, and its value may change
+    eps, quant_group = float(eps), operator.index(quant_group)
     shape, dtype, device = x.shape, x.dtype, x.get_device()
     dim = shape[-1]
     if quant_group and (quant_group < 0 or dim % quant_group):
