@@ -660,14 +660,16 @@ int sm_count()
     return n;
 }
 
-// Launches a walk of `rows` rows, per_cta at a time, on as many CTAs as the GPU holds at once.
+// Launches a walk of `rows` rows, per_cta at a time, on as many CTAs as the GPU holds at once.  `smem_most`
+// is what the kernel's widest rows take: every call sets that limit, so that calls of several host
+// threads, of rows of different widths, never lower it between another one's set and launch.
 template <typename K>
-cudaError_t launch_walk(K kern, const NormArgs &a, int per_cta, int threads, size_t smem, int64_t most,
-                        int64_t *ctas, cudaStream_t st)
+cudaError_t launch_walk(K kern, const NormArgs &a, int per_cta, int threads, size_t smem,
+                        size_t smem_most, int64_t most, int64_t *ctas, cudaStream_t st)
 {
     cudaError_t e;
     if (smem > 40 * 1024) {   // with the static part this may pass 48 KB
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_most);
         if (e != cudaSuccess) return e;
     }
     int64_t grid = (a.rows + per_cta - 1) / per_cta;
@@ -689,11 +691,15 @@ template <typename T, int VEC, int NV, int TPR, int kMode>
 cudaError_t launch(const NormArgs &a, bool bwd, int threads, float *dw, cudaStream_t st)
 {
     const int per_cta = TPR == 0 ? 1 : kRowThreads / TPR;
-    const size_t slots = sizeof(T) * VEC == 16 ? (size_t)rows_ahead(NV) * NV * threads * 16 : 0;
+    constexpr size_t kSlots = sizeof(T) * VEC == 16 ? (size_t)rows_ahead(NV) * NV * 16 : 0;
+    const size_t slots = kSlots * threads;   // bytes of an operand's ring
+    constexpr size_t kMost = kSlots * (TPR == 0 ? kMaxRowThreads : kRowThreads);
+    static_assert(TPR == 0 || kMost * 3 <= 40 * 1024, "needs no limit of its own");
     if (!bwd) {
         const size_t smem = slots * norm_ops(kMode);
         auto go = [&](auto kern) {
-            return launch_walk(kern, a, per_cta, threads, smem, 1 << 30, nullptr, st);
+            return launch_walk(kern, a, per_cta, threads, smem, kMost * norm_ops(kMode), 1 << 30, nullptr,
+                               st);
         };
         if (!a.quant) return go(rms_norm_kernel<T, VEC, NV, TPR, kMode, kNoQuant>);
         if (a.quant == a.dim) return go(rms_norm_kernel<T, VEC, NV, TPR, kMode, kPerRow>);
@@ -706,7 +712,7 @@ cudaError_t launch(const NormArgs &a, bool bwd, int threads, float *dw, cudaStre
     smem = std::max(smem, part);
     int64_t ctas = 0;
     cudaError_t e = launch_walk(rms_norm_bwd_kernel<T, VEC, NV, TPR, kMode>, a, per_cta, threads,
-                                smem, kBwdCtas, &ctas, st);
+                                smem, kMost * norm_bwd_ops(kMode), kBwdCtas, &ctas, st);
     if (e != cudaSuccess) return e;
     return launch_after(rms_norm_dw_kernel, (a.dim + 31) / 32, 1024, 0, st, a.dw_part, dw, (int)ctas,
                         a.dim);
