@@ -564,7 +564,9 @@ def _on(t, name, shape, dtype, device):
 
 class _Call:
     """A call's device and stream (the device's current stream by default): allocates outputs and
-    workspaces, and keeps their memory from being handed out again while that stream uses it."""
+    workspaces.  What a call on another stream allocates comes from that stream's memory: of the
+    current stream's it could be handed what a kernel still waiting there has to read.  Its outputs
+    are kept from being handed out again while the current stream uses them."""
     __slots__ = ("torch", "x", "device", "handle", "other")
 
     def __init__(self, x, stream):
@@ -583,14 +585,20 @@ class _Call:
     # empty_like and new_empty take half of torch.empty's time
     def like(self, t, dtype=None):
         """Uninitialised, with the shape of t, which is contiguous."""
-        return self._used(self.torch.empty_like(t, dtype=dtype))
+        if self.other is None:
+            return self.torch.empty_like(t, dtype=dtype)
+        return self._on_other(lambda: self.torch.empty_like(t, dtype=dtype))
 
     def empty(self, shape, dtype):
-        return self._used(self.x.new_empty(shape, dtype=dtype))
+        if self.other is None:
+            return self.x.new_empty(shape, dtype=dtype)
+        return self._on_other(lambda: self.x.new_empty(shape, dtype=dtype))
 
-    def _used(self, t):
-        if self.other is not None:
-            t.record_stream(self.other)
+    def _on_other(self, make):
+        cuda = self.torch.cuda
+        with cuda.stream(self.other):
+            t = make()
+        t.record_stream(cuda.current_stream(self.device))
         return t
 
     def workspace(self, given, size):
