@@ -50,7 +50,7 @@ struct GradSmem {
         m1 = ds + P * kpitch;
         m2 = m1 + kSpan * mpitch;
         vec = m2 + kSpan * mpitch;
-        total = vec + 7 * kSpan * 4;
+        total = vec + 8 * kSpan * 4;
     }
 };
 __device__ __forceinline__ uint32_t swizzled(int row, int pitch, int piece)
@@ -77,7 +77,8 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
     const uint32_t base = smem_u32(smem);
     float *vec = reinterpret_cast<float *>(smem + lay.vec);
     float *cs = vec, *ek = vec + kSpan, *sw = vec + 2 * kSpan, *eq = vec + 3 * kSpan,
-          *rks = vec + 4 * kSpan, *rqs = vec + 5 * kSpan, *kb = vec + 6 * kSpan;
+          *rks = vec + 4 * kSpan, *rqs = vec + 5 * kSpan, *kb = vec + 6 * kSpan,
+          *cl = vec + 7 * kSpan;
 
     const bf16 *kg = static_cast<const bf16 *>(a.k) + (row0 * a.G + g) * N;
     const bf16 *qg = static_cast<const bf16 *>(a.q) + (row0 * a.G + g) * N;
@@ -149,30 +150,43 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
                                        swizzled(i / (N / 8), lay.kpitch, i % (N / 8))) = o;
         }
         if (warp == 0) {   // the span's decays: lane has tokens lane and lane + 32
-            float gt[2], beta[2];
+            // running sums of g in two floats, as the forward's kernels take them
+            float hi[2], lo[2], beta[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int t = lane + 32 * x;
                 const int64_t at = (row0 + t) * H + h;
-                gt[x] = t < len && a.g ? a.g[at] : 0.f;
+                hi[x] = t < len && a.g ? a.g[at] : 0.f;
+                lo[x] = 0.f;
                 beta[x] = t < len ? a.beta[at] : 0.f;
-                if (gt[x] < -200.f) gt[x] = -200.f;
+                if (hi[x] < -200.f) hi[x] = -200.f;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const float up = __shfl_up_sync(0xffffffffu, gt[x], o);
-                    if (lane >= o) gt[x] += up;
+                    const float up = __shfl_up_sync(0xffffffffu, hi[x], o);
+                    const float ul = __shfl_up_sync(0xffffffffu, lo[x], o);
+                    if (lane >= o) {
+                        float e;
+                        two_sum(hi[x], up, hi[x], e);
+                        lo[x] += ul + e;
+                    }
                 }
             }
-            gt[1] += __shfl_sync(0xffffffffu, gt[0], 31);
-            const float end = __shfl_sync(0xffffffffu, gt[1], 31);
+            const float mid = __shfl_sync(0xffffffffu, hi[0], 31);
+            const float midl = __shfl_sync(0xffffffffu, lo[0], 31);
+            float e;
+            two_sum(hi[1], mid, hi[1], e);
+            lo[1] += midl + e;
+            const float end = __shfl_sync(0xffffffffu, hi[1], 31);
+            const float endl = __shfl_sync(0xffffffffu, lo[1], 31);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int t = lane + 32 * x;
                 const bool on = t < len;
-                const float e = __expf(gt[x]);
-                cs[t] = gt[x];
+                const float e = __expf(hi[x] + lo[x]);
+                cs[t] = hi[x];
+                cl[t] = lo[x];
                 ek[t] = on ? e * rks[t] : 0.f;
-                sw[t] = on ? __expf(end - gt[x]) * rks[t] * beta[x] : 0.f;
+                sw[t] = on ? __expf((end - hi[x]) + (endl - lo[x])) * rks[t] * beta[x] : 0.f;
                 eq[t] = on ? e * rqs[t] : 0.f;
                 kb[t] = on ? rks[t] * beta[x] : 0.f;
             }
@@ -202,11 +216,11 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int i = mt + lane / 4 + r * 8, j = n * 8 + lane % 4 * 2;
-                    const float f = ri[i], ci = cs[i];
+                    const float f = ri[i], ci = cs[i], li = cl[i];
                     const bool on0 = nh ? j < i : j <= i, on1 = nh ? j + 1 < i : j + 1 <= i;
-                    const float x = on0 ? acc[n][2 * r] * f * __expf(ci - cs[j]) * kb[j] : 0.f;
-                    const float y =
-                        on1 ? acc[n][2 * r + 1] * f * __expf(ci - cs[j + 1]) * kb[j + 1] : 0.f;
+                    const float d0 = (ci - cs[j]) + (li - cl[j]), d1 = (ci - cs[j + 1]) + (li - cl[j + 1]);
+                    const float x = on0 ? acc[n][2 * r] * f * __expf(d0) * kb[j] : 0.f;
+                    const float y = on1 ? acc[n][2 * r + 1] * f * __expf(d1) * kb[j + 1] : 0.f;
                     *reinterpret_cast<uint32_t *>(smem + out + swizzled(i, lay.mpitch, n) + j % 8 * 2) =
                         pack_bf16x2(x, y);
                 }

@@ -52,14 +52,6 @@ __device__ __forceinline__ float warp_sum4(float v)   // over 4 neighbouring lan
     return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
-// a + b = s + err exactly
-__device__ __forceinline__ void two_sum(float a, float b, float &s, float &err)
-{
-    s = a + b;
-    const float bb = s - a;
-    err = (a - (s - bb)) + (b - bb);
-}
-
 // grid: (chunks, batch, G * head runs).  kBwd: also the second part of Att, and beta kept away
 // from 0, where the backward divides by it (a token of beta 1e-20 writes nothing either).
 template <int N, bool kBwd>

@@ -1,5 +1,5 @@
 // Warp-level bf16 matrix products of the gated delta rule's chunked kernels: fragments, the split
-// of a float32 into two bf16 parts, shared-memory tiles.
+// of a float32 into bf16 parts, shared-memory tiles; sums in two floats.
 #pragma once
 
 #include "sm100.cuh"
@@ -32,6 +32,14 @@ __device__ __forceinline__ void stsm4_trans(uint32_t addr, const uint32_t (&r)[4
 {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%4], {%0, %1, %2, %3};"
                  ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(addr) : "memory");
+}
+
+// a + b = s + err exactly
+__device__ __forceinline__ void two_sum(float a, float b, float &s, float &err)
+{
+    s = a + b;
+    const float bb = s - a;
+    err = (a - (s - bb)) + (b - bb);
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }

@@ -102,14 +102,6 @@ __device__ __forceinline__ void bulk_store_wait()
 {
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
-// a + b = s + err exactly
-__device__ __forceinline__ void two_sum(float a, float b, float &s, float &err)
-{
-    s = a + b;
-    const float bb = s - a;
-    err = (a - (s - bb)) + (b - bb);
-}
-
 // A head's gates in a chunk, a warp; lane l has tokens 2 l and 2 l + 1.  First the running sums of g
 // (times log2(e), hi + lo) and beta.
 struct Gates {

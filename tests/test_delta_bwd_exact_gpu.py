@@ -56,3 +56,34 @@ def test_decay_gradient_of_two_tokens(cuda_device, P, N):
     want = torch.exp(g[1]) * beta[0] * (D0 * v[0]).sum(-1) - through_k
     err = (got["dg"][0, 1].double().cpu() - want).norm()
     assert err <= 2.0 ** -20 * want.norm() + 3 * 2.0 ** -18 * through_k.norm()
+
+
+@pytest.mark.parametrize("P,N", [(64, 128), (128, 128), (64, 64)])
+def test_decays_behind_tokens_that_wipe_the_state_out(cuda_device, P, N):
+    """Sixty tokens of g = -200, then fractions of 2^-10: the running sum of g is near -12000, where a
+    float32 keeps steps of 2^-10 only, but the decay between the last tokens is a difference of such
+    sums and has float32's accuracy.  One token (61) writes; dk there is beta exp(g_62 + g_63) D^T v,
+    D the final state's gradient, in exact operands: all that is rounded is dk itself, each value by
+    at most 2^-8 of it, which over the n = H N values' projection on the true ones has a deviation of
+    at most 2^-8 / sqrt(n) (|x|^4 of a normal x is 3); six of them are allowed.  (The sum in one float32
+    is off by 1.27e-3 here.)"""
+    H, L = 64, 64
+    gen = torch.Generator().manual_seed(P + N)
+    n = lambda *s: torch.randn(s, generator=gen)
+    k = n(1, L, H, N)
+    k = (k / k.norm(dim=-1, keepdim=True)).to(BF)
+    v, dfinal = n(1, L, H, P).to(BF), n(1, H, P, N).to(BF).float()
+    g = torch.full((1, L, H), -200.0)
+    g[:, 60], g[:, 61], g[:, 62], g[:, 63] = -0.65 * 2.0 ** -10, 0, -0.7 * 2.0 ** -10, 0
+    beta = torch.zeros(1, L, H)
+    beta[:, 61] = 0.5
+    c = [x.to(cuda_device) for x in (k, k, v, g, beta)]
+    got = ssd.delta_rule_bwd(*c, torch.zeros_like(c[2]), dfinal=dfinal.to(cuda_device))
+    decay = torch.exp(g[0, 62:].double().sum(0))[:, None]
+    want = 0.5 * decay * (dfinal[0].double() * v[0, 61].double()[..., None]).sum(1)   # (H, N)
+    dk = got["dk"][0, 61].double().cpu()
+    along = float((dk * want).sum() / (want * want).sum()) - 1
+    assert abs(along) <= 6 * 2.0 ** -8 * (H * N) ** -0.5
+    # a beta of 0 is taken as 1e-20: |dk| <= |dv| |S|, |dv| <= 1e-20 |D| |k| and |S| <= 0.5 |v|, with values
+    # of D and v below 6: 1e-20 * 6 * 128 * 0.5 * 6 * sqrt(128) < 1e-15
+    assert (got["dk"][0, 62:].abs() <= 1e-15).all()
