@@ -49,8 +49,9 @@ ssd_status check_delta(const ssd_shape *s, const ssd_delta_options *o, bool need
     if (o && o->qk_l2norm != 0 && o->qk_l2norm != 1)
         return api_fail(SSD_ERR_INVALID_ARG, "qk_l2norm must be 0 or 1");
     const int64_t blocks = (s->headdim + 15) / 16;   // of the launch grid, per batch row and head
-    if (s->batch * s->nheads * blocks > 0x7fffffffLL || s->seqlen > (int64_t)1 << 34 ||
-        s->batch * s->nheads * (s->seqlen / 32 + 1) > (int64_t)1 << 36)
+    const int64_t seqlen = need_seq ? s->seqlen : 1;
+    if (s->batch * s->nheads * blocks > 0x7fffffffLL || seqlen > (int64_t)1 << 34 ||
+        s->batch * s->nheads * (seqlen / 32 + 1) > (int64_t)1 << 36)
         return api_fail(SSD_ERR_UNSUPPORTED, "problem too large for one launch grid");
     return SSD_OK;
 }
