@@ -42,7 +42,7 @@ constexpr int C = kDeltaChunk;
 constexpr int kPrepWarps = 4;
 constexpr int kPrepHeads = 16;     // most heads of a group per CTA of the prep kernel
 constexpr int kLoadWarps = 2;      // of a CTA of the chains, behind the warps that compute
-constexpr int kMaxRows = 112;      // of a CTA of the chains: leaves a thread 224 registers
+constexpr int kMaxRows = 112;      // of a CTA of the chains: nine warps, of which a thread has 168 registers
 constexpr float kMinDecay = -200.f;    // exp of it is 0 in float32
 constexpr float kMinBeta = 1e-20f;
 
@@ -206,19 +206,19 @@ delta_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, const int2 *t
     }
 }
 
-// Shared-memory stage of one chunk: K and Q of the group, then per head of the CTA its V (and dO,
-// for the backward), its triangles and its factors.  Rows are 16 bytes longer than their data.
+// Shared-memory stage of one chunk: K and Q of the group, then the head's V (and dO, for the
+// backward), its triangles and its factors.  Rows are 16 bytes longer than their data.
 struct ChainStage {
-    int kpitch, vpitch, tri, vec, state, w, head, total;   // bytes; from tri on offsets in a head's part
+    int kpitch, vpitch, head, tri, vec, state, w, total;   // bytes; from tri on offsets in the head's part
     static constexpr int kTriPitch = C * 2 + 16;
     static constexpr int kTri = C * kTriPitch;
     // bwd: with dO and Att's second part; adjoint: also the state behind a span, and W (in
     // accumulator layout)
-    __host__ __device__ ChainStage(int rows, int N, int heads, bool bwd, bool adjoint = false)
-        : kpitch(N * 2 + 16), vpitch(rows * 2 + 16), tri((bwd ? 2 : 1) * C * (rows * 2 + 16)),
-          vec(tri + (bwd ? 4 : 3) * kTri), state(vec + 512),
+    __host__ __device__ ChainStage(int rows, int N, bool bwd, bool adjoint = false)
+        : kpitch(N * 2 + 16), vpitch(rows * 2 + 16), head(2 * C * kpitch),
+          tri((bwd ? 2 : 1) * C * (rows * 2 + 16)), vec(tri + (bwd ? 4 : 3) * kTri), state(vec + 512),
           w(state + (adjoint ? rows * state_pitch(N) : 0)),
-          head(w + (adjoint ? rows * C * 4 : 0)), total(2 * C * kpitch + heads * head)
+          total(head + w + (adjoint ? rows * C * 4 : 0))
     {
     }
     static __host__ __device__ constexpr int state_pitch(int N) { return N * 4 + 32; }
@@ -231,15 +231,14 @@ __host__ __device__ constexpr bool adjoint_staged(int rows) { return rows == 16;
 // The CTA's share of a launch: see delta_chain_kernel.
 struct ChainSlice {
     int64_t b, seq;
-    int h0, g, pb, heads, rows;
-    __device__ ChainSlice(const DeltaArgs &a, int heads_, int rows_, bool packed)
-        : heads(heads_), rows(rows_)
+    int h, g, pb, rows;
+    __device__ ChainSlice(const DeltaArgs &a, int rows_, bool packed) : rows(rows_)
     {
-        const int splits = a.P / rows, blocks = a.H / heads * splits;
+        const int splits = a.P / rows, blocks = a.H * splits;
         pb = (int)(blockIdx.x % splits) * rows;
-        h0 = (int)(blockIdx.x % blocks) / splits * heads;
+        h = (int)(blockIdx.x % blocks) / splits;
         seq = blockIdx.x / blocks;
-        g = h0 / (a.H / a.G);
+        g = h / (a.H / a.G);
         b = packed ? 0 : seq;
     }
 };
@@ -266,31 +265,28 @@ __device__ __forceinline__ void load_stage(const DeltaArgs &a, const ChainStage 
         cp16(s + r * lay.kpitch + col * 16, kg + off, on);
         cp16(s + (C + r) * lay.kpitch + col * 16, qg + off, on);
     }
-    for (int x = 0; x < w.heads; ++x) {
-        const uint32_t sh = s + 2 * C * lay.kpitch + x * lay.head;
-        const int64_t vat = (row0 * a.H + w.h0 + x) * a.P + w.pb;
-        const bf16 *vg = static_cast<const bf16 *>(a.v) + vat;
-        const int pieces = w.rows / 8;
-        for (int i = tid; i < C * pieces; i += nthr) {
-            const int r = i / pieces, col = i % pieces;
-            const bool on = r < len;
-            const int64_t off = on ? (int64_t)r * a.H * a.P + col * 8 : 0;
-            cp16(sh + r * lay.vpitch + col * 16, vg + off, on);
-            if (kBwd) cp16(sh + (C + r) * lay.vpitch + col * 16, dout + vat + off, on);
-        }
-        const char *item = items + ((w.b * nchunks + c) * a.H + w.h0 + x) * DeltaItem::bytes(kBwd);
-        constexpr int kTris = kBwd ? 4 : 3;
-        for (int i = tid; i < kTris * C * 4 + 32; i += nthr) {
-            if (i < kTris * C * 4) {   // Inv's two parts, Att's: rows of four 16-byte pieces
-                const int m = i / (C * 4), r = i / 4 % C, col = i % 4;
-                const int src = m < 2 ? m * DeltaItem::kTri
-                                      : DeltaItem::kAttHi + (m - 2) * DeltaItem::kTri;
-                cp16(sh + lay.tri + m * ChainStage::kTri + r * ChainStage::kTriPitch + col * 16,
-                     item + src + r * C * 2 + col * 16, true);
-            } else {
-                const int j = i - kTris * C * 4;
-                cp16(sh + lay.vec + j * 16, item + DeltaItem::kVec + j * 16, true);
-            }
+    const uint32_t sh = s + lay.head;
+    const int64_t vat = (row0 * a.H + w.h) * a.P + w.pb;
+    const bf16 *vg = static_cast<const bf16 *>(a.v) + vat;
+    const int pieces = w.rows / 8;
+    for (int i = tid; i < C * pieces; i += nthr) {
+        const int r = i / pieces, col = i % pieces;
+        const bool on = r < len;
+        const int64_t off = on ? (int64_t)r * a.H * a.P + col * 8 : 0;
+        cp16(sh + r * lay.vpitch + col * 16, vg + off, on);
+        if (kBwd) cp16(sh + (C + r) * lay.vpitch + col * 16, dout + vat + off, on);
+    }
+    const char *item = items + ((w.b * nchunks + c) * a.H + w.h) * DeltaItem::bytes(kBwd);
+    constexpr int kTris = kBwd ? 4 : 3;
+    for (int i = tid; i < kTris * C * 4 + 32; i += nthr) {
+        if (i < kTris * C * 4) {   // Inv's two parts, Att's: rows of four 16-byte pieces
+            const int m = i / (C * 4), r = i / 4 % C, col = i % 4;
+            const int src = m < 2 ? m * DeltaItem::kTri : DeltaItem::kAttHi + (m - 2) * DeltaItem::kTri;
+            cp16(sh + lay.tri + m * ChainStage::kTri + r * ChainStage::kTriPitch + col * 16,
+                 item + src + r * C * 2 + col * 16, true);
+        } else {
+            const int j = i - kTris * C * 4;
+            cp16(sh + lay.vec + j * 16, item + DeltaItem::kVec + j * 16, true);
         }
     }
 }
@@ -371,13 +367,13 @@ template <int kDots> __device__ __forceinline__ void fold_tokens(float (&v)[kDot
     }
 }
 
-// A CTA has `heads` heads of one group and of each `rows` rows p: heads * rows / 16 warps.
-// grid: (sequences * H / heads * P / rows).  kBwd: the forward once more for the backward, which
-// keeps the state every 64 tokens, W, and the dot products of o and its gradient instead of o.
+// A CTA has `rows` rows p of a head: rows / 16 warps.  grid: (sequences * H * P / rows).  kBwd: the
+// forward once more for the backward, which keeps the state every 64 tokens, W, and the dot products of
+// o and its gradient instead of o.
 template <int N, bool kBwd>
 __global__ void __launch_bounds__((kMaxRows / 16 + kLoadWarps) * 32)
 delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64_t nchunks,
-                   const int2 *tab, const int32_t *cstart, const int *status, int heads, int rows)
+                   const int2 *tab, const int32_t *cstart, const int *status, int rows)
 {
     extern __shared__ __align__(128) char smem[];
     if (status && *status) {
@@ -386,16 +382,15 @@ delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64
     }
     constexpr int NT = N / 8;
     const int P = a.P;
-    const ChainStage lay(rows, N, heads, kBwd);
-    const ChainSlice slice(a, heads, rows, cstart != nullptr);
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const int hl = warp / (rows / 16), pl = warp % (rows / 16) * 16;   // this warp's head, rows
-    const int p0 = slice.pb + pl, h = slice.h0 + hl;
+    const ChainStage lay(rows, N, kBwd);
+    const ChainSlice slice(a, rows, cstart != nullptr);
+    const int tid = threadIdx.x, lane = tid % 32, pl = tid / 32 * 16;   // this warp's rows of the CTA's
+    const int p0 = slice.pb + pl, h = slice.h;
     const int64_t b = slice.b, seq = slice.seq;
     const int64_t c_begin = cstart ? cstart[seq] : 0, c_end = cstart ? cstart[seq + 1] : nchunks;
 
     const uint32_t base = smem_u32(smem);
-    if (hl >= heads) {   // the load warps: a chunk ahead of the others
+    if (pl >= rows) {   // the load warps: a chunk ahead of the others
         wait_before();   // the others read nothing of the kernel before
         for (int64_t c = c_begin; c <= c_end; ++c) {
             if (c < c_end)
@@ -420,10 +415,10 @@ delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64
         __syncthreads();   // this chunk has arrived; everyone is done with the other stage
 
         const uint32_t ks = base + stage * lay.total, qs = ks + C * lay.kpitch;
-        const uint32_t vs = qs + C * lay.kpitch + hl * lay.head;
+        const uint32_t vs = ks + lay.head;
         const uint32_t inv = vs + lay.tri, att = inv + 2 * ChainStage::kTri;
-        const float *vec = reinterpret_cast<const float *>(
-            smem + stage * lay.total + 2 * C * lay.kpitch + hl * lay.head + lay.vec);
+        const float *vec =
+            reinterpret_cast<const float *>(smem + stage * lay.total + lay.head + lay.vec);
         const int64_t item = (b * nchunks + c) * a.H + h;
         if (kBwd && c % 2 == 0)
             store_acc<N>(w.states + ((b * (w.n64 + 1) + c / 2) * a.H + h) * P * N + pn, S);
@@ -607,34 +602,33 @@ delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64
 template <int N>
 __global__ void __launch_bounds__((kMaxRows / 16 + kLoadWarps) * 32)
 delta_adjoint_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64_t nchunks,
-                     int heads, int rows)
+                     int rows)
 {
     extern __shared__ __align__(128) char smem[];
     wait_before();
     constexpr int NT = N / 8;
     const int P = a.P;
     const bool staged = adjoint_staged(rows);
-    const ChainStage lay(rows, N, heads, true, staged);
-    const ChainSlice slice(a, heads, rows, false);
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const int hl = warp / (rows / 16), pl = warp % (rows / 16) * 16;
-    const int p0 = slice.pb + pl, h = slice.h0 + hl;
+    const ChainStage lay(rows, N, true, staged);
+    const ChainSlice slice(a, rows, false);
+    const int tid = threadIdx.x, lane = tid % 32, pl = tid / 32 * 16;
+    const int p0 = slice.pb + pl, h = slice.h;
     const int64_t b = slice.b;
 
     const uint32_t base = smem_u32(smem);
-    if (hl >= heads) {   // the load warps
+    if (pl >= rows) {   // the load warps
         for (int64_t c = nchunks - 1; c >= -1; --c) {
             const uint32_t to = base + ((nchunks - 1 - c) & 1) * lay.total;
             if (c >= 0) load_stage<N, true>(a, lay, slice, items, w.dout, nchunks, nullptr, c, to);
-            if (c >= 0 && staged) {   // one head, 16 rows
+            if (c >= 0 && staged) {   // 16 rows
                 const int i0 = tid % (kLoadWarps * 32);
-                const uint32_t head = to + 2 * C * lay.kpitch;
-                const int64_t item = (b * nchunks + c) * a.H + slice.h0;
+                const uint32_t head = to + lay.head;
+                const int64_t item = (b * nchunks + c) * a.H + h;
                 const float *wf = w.wfrag + (item * (P / 16) + slice.pb / 16) * (16 * C);
                 for (int i = i0; i < 16 * C / 4; i += kLoadWarps * 32)
                     cp16(head + lay.w + i * 16, wf + i * 4, true);
                 if (c % 2 == 1 || c == nchunks - 1) {
-                    const float *sn = w.states + (((b * (w.n64 + 1) + c / 2 + 1) * a.H + slice.h0) * P +
+                    const float *sn = w.states + (((b * (w.n64 + 1) + c / 2 + 1) * a.H + h) * P +
                                                   slice.pb) * (int64_t)N;
                     for (int i = i0; i < 16 * N / 4; i += kLoadWarps * 32)
                         cp16(head + lay.state + i / (N / 4) * lay.state_pitch(N) + i % (N / 4) * 16,
@@ -659,9 +653,9 @@ delta_adjoint_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int
         __syncthreads();
 
         const uint32_t ks = base + stage * lay.total, qs = ks + C * lay.kpitch;
-        const uint32_t vs = qs + C * lay.kpitch + hl * lay.head;
+        const uint32_t vs = ks + lay.head;
         const uint32_t inv = vs + lay.tri, att = inv + 2 * ChainStage::kTri;
-        const char *part = smem + stage * lay.total + 2 * C * lay.kpitch + hl * lay.head;
+        const char *part = smem + stage * lay.total + lay.head;
         const float *vec = reinterpret_cast<const float *>(part + lay.vec);
         const int64_t item = (b * nchunks + c) * a.H + h;
         const int64_t tile = item * (P / 16) + p0 / 16;
@@ -890,13 +884,13 @@ cudaError_t launch_delta_chain(const DeltaArgs &a, const DeltaBwd *bwd, const ch
                                const int *status, cudaStream_t st)
 {
     const int64_t nseq = cstart ? a.nseq : a.batch;
-    const int heads = 1, rows = chain_rows(a, nseq);
-    const unsigned grid = (unsigned)(nseq * (a.H / heads) * (a.P / rows));
-    const unsigned threads = (unsigned)((heads * rows / 16 + kLoadWarps) * 32);
-    const int smem = 2 * ChainStage(rows, a.N, heads, bwd != nullptr).total;
+    const int rows = chain_rows(a, nseq);
+    const unsigned grid = (unsigned)(nseq * a.H * (a.P / rows));
+    const unsigned threads = (unsigned)((rows / 16 + kLoadWarps) * 32);
+    const int smem = 2 * ChainStage(rows, a.N, bwd != nullptr).total;
     const DeltaBwd w = bwd ? *bwd : DeltaBwd{};
     auto go = [&](auto kern) {
-        return launch_after(kern, grid, threads, smem, st, a, w, items, nchunks, tab, cstart, status, heads, rows);
+        return launch_after(kern, grid, threads, smem, st, a, w, items, nchunks, tab, cstart, status, rows);
     };
     if (bwd) return a.N == 128 ? go(delta_chain_kernel<128, true>) : go(delta_chain_kernel<64, true>);
     return a.N == 128 ? go(delta_chain_kernel<128, false>) : go(delta_chain_kernel<64, false>);
@@ -905,12 +899,12 @@ cudaError_t launch_delta_chain(const DeltaArgs &a, const DeltaBwd *bwd, const ch
 cudaError_t launch_delta_adjoint(const DeltaArgs &a, const DeltaBwd &w, const char *items,
                                  int64_t nchunks, cudaStream_t st)
 {
-    const int heads = 1, rows = chain_rows(a, a.batch);
-    const unsigned grid = (unsigned)(a.batch * (a.H / heads) * (a.P / rows));
-    const unsigned threads = (unsigned)((heads * rows / 16 + kLoadWarps) * 32);
-    const int smem = 2 * ChainStage(rows, a.N, heads, true, adjoint_staged(rows)).total;
+    const int rows = chain_rows(a, a.batch);
+    const unsigned grid = (unsigned)(a.batch * a.H * (a.P / rows));
+    const unsigned threads = (unsigned)((rows / 16 + kLoadWarps) * 32);
+    const int smem = 2 * ChainStage(rows, a.N, true, adjoint_staged(rows)).total;
     auto go = [&](auto kern) {
-        return launch_after(kern, grid, threads, smem, st, a, w, items, nchunks, heads, rows);
+        return launch_after(kern, grid, threads, smem, st, a, w, items, nchunks, rows);
     };
     return a.N == 128 ? go(delta_adjoint_kernel<128>) : go(delta_adjoint_kernel<64>);
 }
