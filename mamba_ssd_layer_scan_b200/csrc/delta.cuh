@@ -95,22 +95,18 @@ bool delta_chunk_supported(bool is_bf16, int P, int N);
 // The chunked form on tcgen05 (delta_tc.cu): bf16, P and N 64 or 128.  A bounded wait that gives up
 // sets a bit of `status`, the workspace's status word.
 constexpr int kDeltaTcChunk = 64;
-constexpr int kDeltaTcItem = 19 * 1024;   // bytes of the workspace per chunk and head
+constexpr int kDeltaTcItem = 25 * 1024;   // bytes of the workspace per chunk and head
 bool delta_tc_supported(int P, int N);
 cudaError_t launch_delta_tc(const DeltaArgs &a, char *items, int64_t nchunks, const int2 *tab,
                             const int32_t *cstart, int *status, cudaStream_t st);
 
-// What delta_prep_kernel leaves of one chunk of one head, 6.5 KB in the workspace (8.5 KB with the
-// second part of att, for the backward).  Row-major 32 x 32 bf16 triangles in two parts each.
+// What delta_prep_kernel leaves of one chunk of one head, 8.5 KB in the workspace: row-major 32 x 32
+// bf16 triangles in two parts each.
 struct DeltaItem {
     static constexpr int kTri = kDeltaChunk * kDeltaChunk * 2;   // bytes of one part
     static constexpr int kInvHi = 0, kInvLo = kTri, kVec = 2 * kTri;
-    static constexpr int kAttHi = kVec + 512, kAttLo = kAttHi + kTri;
     // floats at kVec: ek[32], sw[32], eq[32], the chunk's decay
-    static __host__ __device__ constexpr int bytes(bool two_parts)
-    {
-        return two_parts ? kAttLo + kTri : kAttLo;
-    }
+    static constexpr int kAttHi = kVec + 512, kAttLo = kAttHi + kTri, kBytes = kAttLo + kTri;
 };
 
 cudaError_t launch_delta_prep(const DeltaArgs &a, char *items, bool for_backward, int64_t nchunks,

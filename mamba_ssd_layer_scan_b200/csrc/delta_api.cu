@@ -36,7 +36,7 @@ size_t items_bytes(const ssd_shape *s, Path p, int64_t chunks)
 {
     const size_t items = (size_t)(s->batch * chunks * s->nheads);
     return p == Path::kTc ? items * kDeltaTcItem
-                          : p == Path::kChunk ? items * DeltaItem::bytes(false) : 0;
+                          : p == Path::kChunk ? items * DeltaItem::kBytes : 0;
 }
 
 ssd_status check_delta(const ssd_shape *s, const ssd_delta_options *o, bool need_seq)
@@ -145,7 +145,7 @@ BwdWs bwd_ws(const ssd_shape *s)
         at += api_round256(bytes);
         return here;
     };
-    w.items = take(items * DeltaItem::bytes(true));
+    w.items = take(items * DeltaItem::kBytes);
     w.states = take((spans + (size_t)s->batch * H) * PN * 4);
     w.dstates = take(spans * PN * 2);
     w.wfrag = take(items * (size_t)s->headdim * kDeltaChunk * 4);

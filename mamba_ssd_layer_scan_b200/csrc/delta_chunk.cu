@@ -17,10 +17,9 @@
 // of K, Q, V and the triangles, which two more warps bring one chunk ahead by cp.async (with the
 // copies issued by the computing warps a chunk took 3.9 us for 2.3, at 2 x 2048 tokens x 24 heads).
 //
-// Accuracy: K, Q and V enter as they are; the state, the residual, W and Inv, which are float32,
-// enter as two bf16 parts each (2^-16), so that the state is carried to float32's usual accuracy:
-// 146 of the 184 matrix instructions per warp and chunk (P = 64, N = 128).  The output, rounded to
-// bf16 at once, takes the first parts only.
+// Accuracy: K, Q and V enter as they are; the state, the residual, W, Inv and Att, which are float32,
+// enter as two bf16 parts each (2^-17 of one is left), so that final states are 3e-6 off (float32 sums
+// alone leave 3e-7) and the output by little more than its own rounding.
 // The backward's dg is a small difference of these products: what two parts leave of the values that
 // are written, of dS in dS K^T and of W in Att W came to 1e-5 and more of dg for one call in eighty of a
 // few tokens and heads (2.7e-5 at worst of 1800 such calls).  There these take three parts, and that is
@@ -52,8 +51,8 @@ __device__ __forceinline__ float warp_sum4(float v)   // over 4 neighbouring lan
     return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
-// grid: (chunks, batch, G * head runs).  kBwd: also the second part of Att, and beta kept away
-// from 0, where the backward divides by it (a token of beta 1e-20 writes nothing either).
+// grid: (chunks, batch, G * head runs).  kBwd: beta kept away from 0, where the backward divides by it
+// (a token of beta 1e-20 writes nothing either).
 template <int N, bool kBwd>
 __global__ void __launch_bounds__(kPrepWarps * 32)
 delta_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, const int2 *tab, int run_heads)
@@ -153,7 +152,7 @@ delta_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, const int2 *t
         const float cs_end = __shfl_sync(0xffffffffu, cs, 31);
         const float cl_end = __shfl_sync(0xffffffffu, cl, 31);
         const float e = __expf(cs + cl);
-        char *item = items + ((b * nchunks + c) * a.H + h) * DeltaItem::bytes(kBwd);
+        char *item = items + ((b * nchunks + c) * a.H + h) * DeltaItem::kBytes;
         float *vec = reinterpret_cast<float *>(item + DeltaItem::kVec);
         vec[lane] = on ? e * rk : 0.f;
         vec[C + lane] = on ? __expf((cs_end - cs) + (cl_end - cl)) * rk * beta : 0.f;
@@ -201,7 +200,7 @@ delta_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, const int2 *t
             *reinterpret_cast<uint32_t *>(item + DeltaItem::kInvLo + off) = lo;
             split2(odd ? ao : att[i], odd ? att[i + 1] : ao, hi, lo);
             *reinterpret_cast<uint32_t *>(item + DeltaItem::kAttHi + off) = hi;
-            if (kBwd) *reinterpret_cast<uint32_t *>(item + DeltaItem::kAttLo + off) = lo;
+            *reinterpret_cast<uint32_t *>(item + DeltaItem::kAttLo + off) = lo;
         }
     }
 }
@@ -212,11 +211,11 @@ struct ChainStage {
     int kpitch, vpitch, head, tri, vec, state, w, total;   // bytes; from tri on offsets in the head's part
     static constexpr int kTriPitch = C * 2 + 16;
     static constexpr int kTri = C * kTriPitch;
-    // bwd: with dO and Att's second part; adjoint: also the state behind a span, and W (in
+    // bwd: with dO; adjoint: also the state behind a span, and W (in
     // accumulator layout)
     __host__ __device__ ChainStage(int rows, int N, bool bwd, bool adjoint = false)
         : kpitch(N * 2 + 16), vpitch(rows * 2 + 16), head(2 * C * kpitch),
-          tri((bwd ? 2 : 1) * C * (rows * 2 + 16)), vec(tri + (bwd ? 4 : 3) * kTri), state(vec + 512),
+          tri((bwd ? 2 : 1) * C * (rows * 2 + 16)), vec(tri + 4 * kTri), state(vec + 512),
           w(state + (adjoint ? rows * state_pitch(N) : 0)),
           total(head + w + (adjoint ? rows * C * 4 : 0))
     {
@@ -276,8 +275,8 @@ __device__ __forceinline__ void load_stage(const DeltaArgs &a, const ChainStage 
         cp16(sh + r * lay.vpitch + col * 16, vg + off, on);
         if (kBwd) cp16(sh + (C + r) * lay.vpitch + col * 16, dout + vat + off, on);
     }
-    const char *item = items + ((w.b * nchunks + c) * a.H + w.h) * DeltaItem::bytes(kBwd);
-    constexpr int kTris = kBwd ? 4 : 3;
+    const char *item = items + ((w.b * nchunks + c) * a.H + w.h) * DeltaItem::kBytes;
+    constexpr int kTris = 4;
     for (int i = tid; i < kTris * C * 4 + 32; i += nthr) {
         if (i < kTris * C * 4) {   // Inv's two parts, Att's: rows of four 16-byte pieces
             const int m = i / (C * 4), r = i / 4 % C, col = i % 4;
@@ -439,10 +438,8 @@ delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64
                 ldsm4(fb, qs + (n * 16 + row_nn) * lay.kpitch + s * 32 + col_nn);
                 mma_16816(O[2 * n], hi, fb[0], fb[1]);
                 mma_16816(O[2 * n + 1], hi, fb[2], fb[3]);
-                if (kBwd) {
-                    mma_16816(O[2 * n], lo, fb[0], fb[1]);
-                    mma_16816(O[2 * n + 1], lo, fb[2], fb[3]);
-                }
+                mma_16816(O[2 * n], lo, fb[0], fb[1]);
+                mma_16816(O[2 * n + 1], lo, fb[2], fb[3]);
             }
         }
         // R = V - e K S^T, in place of S K^T; the output's part from the state takes its factor
@@ -497,7 +494,7 @@ delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 if constexpr (kBwd) split_a(W[2 * s], W[2 * s + 1], hi[s], lo[s], rest[s]);
-                else round_a(W[2 * s], W[2 * s + 1], hi[s]);
+                else split_a(W[2 * s], W[2 * s + 1], hi[s], lo[s]);
             }
 #pragma unroll
             for (int n = 0; n < 2; ++n)
@@ -507,13 +504,13 @@ delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64
                     const uint32_t at =
                         att + (n * 16 + row_nn) * ChainStage::kTriPitch + s * 32 + col_nn;
                     ldsm4(fb, at);
-                    if (kBwd) ldsm4(fl, at + ChainStage::kTri);
+                    ldsm4(fl, at + ChainStage::kTri);
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
                         mma_16816(O[2 * n + m], hi[s], fb[2 * m], fb[2 * m + 1]);
-                        if (kBwd) {
-                            mma_16816(O[2 * n + m], lo[s], fb[2 * m], fb[2 * m + 1]);
-                            mma_16816(O[2 * n + m], hi[s], fl[2 * m], fl[2 * m + 1]);
+                        mma_16816(O[2 * n + m], lo[s], fb[2 * m], fb[2 * m + 1]);
+                        mma_16816(O[2 * n + m], hi[s], fl[2 * m], fl[2 * m + 1]);
+                        if constexpr (kBwd) {
                             mma_16816(O[2 * n + m], rest[s], fb[2 * m], fb[2 * m + 1]);
                             mma_16816(O[2 * n + m], lo[s], fl[2 * m], fl[2 * m + 1]);
                         }

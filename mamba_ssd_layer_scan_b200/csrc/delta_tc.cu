@@ -8,9 +8,12 @@
 // one head of 128, or two heads of 64 of one group -- through a sequence.  Every product has p on
 // the accumulator's lanes, so each result, taken from TMEM by the thread that owns the row and
 // written back as bf16, is the next product's A operand; the B operands (K, Q, Inv, Att) lie in
-// shared memory, K serving both as rows (X) and as columns (S').  S, R and sw W enter as two bf16
-// parts and Inv as two, which keeps the carried state at float32's usual accuracy; the output
-// takes first parts only.  The state itself stays in registers, float32.  Two heads that share a
+// shared memory, K serving both as rows (X) and as columns (S').  S, R, sw W and Inv enter as two bf16
+// parts each, so that final states are 3e-6 off (float32 sums alone leave 3e-7).  Att W, which goes to the
+// output alone, is a product of float32 operands cut to 10 bits, W read where its product left it.  (Of
+// bf16 operands it was off by as much as the output's own rounding for each of the two, 0.0033 for 0.0017
+// in all; in two bf16 parts each it took half as much again and the parts' making: packed 16384 tokens x
+// 80 heads 487 us, this form 446, bf16 420.)  The state itself stays in registers, float32.  Two heads that share a
 // CTA multiply all 128 rows by each head's triangles and read their own result: 2 x 64 columns
 // cost the same as a block-diagonal product, and what is not finite in one head stays there.
 //
@@ -31,14 +34,18 @@ constexpr int kTile = kC * 128;        // bytes of a 64 x 64 bf16 tile, rows 128
 constexpr float kLog2e = 1.4426950408889634f;   // and what it leaves of log2(e)
 constexpr float kLog2eLow = 1.9259629911266175e-8f;
 
+// A float cut to 10 bits of mantissa is smaller by a quantity spread evenly over [0, 2^(e-10)): in a sum
+// by 2^-11 ln 2 of it, with mantissas as evenly spread as logarithms are.  Att and W are both cut.
+constexpr float kCutBoth = 1.f + 2 * 0.693147f / 2048;
+
 template <int I> struct Int { static constexpr int value = I; };
 
 // ---------------------------------------------------------------- the triangles
 // A triangle, 64 x 64 bf16 in 6 KB: columns 0-31 of all rows, then columns 32-63 of rows 32-63, in
-// rows of 64 bytes, 64-byte swizzled.  An item, per chunk and head: Inv in two parts, Att, and the
-// factors -ek, sw, eq (64 floats each) and E (four times).
-constexpr int kMat = 6 * 1024, kMatRight = 4 * 1024;
-constexpr int kItemAtt = 2 * kMat, kItemVec = 3 * kMat, kVecFloats = 3 * kC + 4;
+// rows of 64 bytes, 64-byte swizzled; in float32 (Att) 12 KB, in rows of 128 bytes, 128-byte swizzled.  An item, per chunk and head: Inv in two parts, Att,
+// and the factors -ek, sw, eq (64 floats each) and E (four times).
+constexpr int kMat = 6 * 1024, kMatRight = 4 * 1024, kAttRight = 8 * 1024;
+constexpr int kMats = 4 * kMat, kItemAtt = 2 * kMat, kItemVec = kMats, kVecFloats = 3 * kC + 4;
 constexpr int kItem = kDeltaTcItem, kItemUsed = kItemVec + kVecFloats * 4;
 static_assert(kItemUsed <= kItem && kItemUsed % 16 == 0 && kItem % 1024 == 0, "an item");
 // Byte offset of the 16-byte piece `c` (8 columns) of row `r` of a triangle.
@@ -46,11 +53,17 @@ __device__ __forceinline__ uint32_t tri_at(int r, int c)
 {
     return (c < 4 ? r * 64 : kMatRight + (r - 32) * 64) + (((c ^ (r >> 1)) & 3) << 4);
 }
+// Of the 8 columns `n` of a row of the one in float32, from the place of the row's first 8 (128-byte
+// aligned apart from the swizzle).
+__device__ __forceinline__ uint32_t att_at(uint32_t first, int n)
+{
+    return (first ^ ((n & 3) << 5)) + (n < 4 ? 0 : kAttRight - 32 * 128);
+}
 
 constexpr int kPrepWarps = 4, kPrepThreads = 2 * kPrepWarps * 32, kPrepQuad = 4;
 // what the builders need of a head: log2(e) cs and its low part, both negated, kb, w
 constexpr int kCs = 0, kCl = kC, kKb = 2 * kC, kW = 3 * kC, kGateFloats = 4 * kC;
-constexpr int kPrepGates = 2 * 3 * kMat,   // K and Q lie there first
+constexpr int kPrepGates = 2 * kMats,   // K and Q lie there first
               kPrepNorms = kPrepGates + 2 * kPrepQuad * kGateFloats * 4,
               kPrepSmem = kPrepNorms + 2 * kC * 4;
 static_assert(kPrepGates >= 4 * kTile, "K and Q of 128 columns");
@@ -194,12 +207,16 @@ __device__ __forceinline__ void build_rows(const float (&g)[8][4], int b, const 
                                            uint32_t gates, uint32_t tri)
 {
     const int lane = threadIdx.x % 32, j0 = 2 * (lane % 4);
+    const bool odd = lane & 4;   // this lane's rows
     int r[2];
+    uint32_t to[2];   // Att's: of the first of two values, the second's is to ^ 4
     float ri[2], c[2], l[2];
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
         r[y] = b * 16 + lane / 4 + y * 8;
-        ri[y] = norms[(kAtt ? kC : 0) + r[y]];
+        // rows r and r ^ 1 have their 16-byte pieces in the same banks: they store in opposite orders
+        to[y] = tri + kItemAtt + r[y] * 128 + (((j0 / 4 ^ r[y]) & 7) << 4) + (j0 % 4 + r[y] % 2) * 4;
+        ri[y] = kAtt ? norms[kC + r[y]] * kCutBoth : norms[r[y]];
         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(c[y]) : "r"(gates + (kCs + r[y]) * 4));
         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(l[y]) : "r"(gates + (kCl + r[y]) * 4));
     }
@@ -224,12 +241,13 @@ __device__ __forceinline__ void build_rows(const float (&g)[8][4], int b, const 
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const uint64_t v = mul2(mul2(pair(g[n][2 * y], g[n][2 * y + 1]), w), u[y]);
-                    const uint32_t at = tri + tri_at(r[y], n) + j0 * 2;
                     if constexpr (kAtt) {
                         float x, z;
                         unpair(v, x, z);
-                        sts32(at + kItemAtt, pack_bf16x2(x, z));
+                        sts32(att_at(to[y], n), __float_as_uint(odd ? z : x));
+                        sts32(att_at(to[y], n) ^ 4, __float_as_uint(odd ? x : z));
                     } else {
+                        const uint32_t at = tri + tri_at(r[y], n) + j0 * 2;
                         uint32_t hi, lo;
                         split2(v, hi, lo);
                         sts32(at, hi);
@@ -254,10 +272,12 @@ __device__ __forceinline__ void build_rows(const float (&g)[8][4], int b, const 
                     const int end = r[y] + (kAtt ? 1 : 0);   // columns before it
                     x = j < end ? x : 0.f;
                     z = j + 1 < end ? z : 0.f;
-                    if constexpr (kAtt)
-                        sts32(tri + kItemAtt + tri_at(r[y], n) + j0 * 2, pack_bf16x2(x, z));
-                    else
+                    if constexpr (kAtt) {
+                        sts32(att_at(to[y], n), __float_as_uint(odd ? z : x));
+                        sts32(att_at(to[y], n) ^ 4, __float_as_uint(odd ? x : z));
+                    } else {
                         sts64(tri + n % 2 * kMat + tri_at(r[y], 2 * bb + j0 / 4) + j0 % 4 * 4, x, z);
+                    }
                 }
             }
         }
@@ -481,8 +501,8 @@ delta_tc_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, int run_he
         __syncthreads();
         const uint32_t gates = base + gates_of(hq) + (hp - hq) * kGateFloats * 4;
         for (int x = 0; x < here; ++x) {
-            if (att) build_rows<true>(g, blk, norms, gates + x * kGateFloats * 4, base + x * 3 * kMat);
-            else build_rows<false>(g, blk, norms, gates + x * kGateFloats * 4, base + x * 3 * kMat);
+            if (att) build_rows<true>(g, blk, norms, gates + x * kGateFloats * 4, base + x * kMats);
+            else build_rows<false>(g, blk, norms, gates + x * kGateFloats * 4, base + x * kMats);
         }
         if (att) {
             if (hp > hq || hp + 2 >= h_end) {
@@ -492,13 +512,13 @@ delta_tc_prep_kernel(const DeltaArgs a, char *items, int64_t nchunks, int run_he
             }
         } else {
             named_bar_sync(3, kPrepWarps * 32);
-            if (warp / 2 < here) solve_head(base + warp / 2 * 3 * kMat, warp % 2, 1 + warp / 2);
+            if (warp / 2 < here) solve_head(base + warp / 2 * kMats, warp % 2, 1 + warp / 2);
         }
         fence_async_smem();
         __syncthreads();
         if (tid == 0)
             for (int x = 0; x < here; ++x)
-                bulk_store(items + (item0 + hp + x) * kItem, base + x * 3 * kMat, 3 * kMat);
+                bulk_store(items + (item0 + hp + x) * kItem, base + x * kMats, kMats);
     }
     if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
@@ -509,8 +529,8 @@ constexpr int kTcThreads = (kMma + 4) * 32;
 constexpr int kKqStages = 2;
 
 // TMEM columns.  S's operand parts share the columns of its update; W of the first head those of
-// X; W of the second head and its Att product one block.  W's bf16 rounding lies in X's columns
-// once W has been read.
+// X.  The Att product of the second head takes the place of the operands of the state's update, once
+// that is done.
 constexpr uint32_t kColS = 0, kColX = 128, kColW1 = 192, kColAw = 256, kColQ = 320, kColVt = 384,
                    kColOp = 448;
 
@@ -552,7 +572,7 @@ __device__ __forceinline__ void row_warps(const DeltaArgs &a, TcBars &bar, uint3
     const int x = here ? r / P : 0, h = h0 + x, p = r % P;
     const uint32_t t0 = tmem + ((uint32_t)quad << 21);
     const uint32_t col_w = t0 + (x ? kColW1 : kColX) + half * 32;
-    const uint32_t col_aw = t0 + (x ? kColW1 : kColAw) + half * 32;
+    const uint32_t col_aw = t0 + (x ? kColOp : kColAw) + half * 32;
     volatile int *abort = &bar.abort;
 
     uint64_t S[NS / 2];   // pairs of columns
@@ -672,7 +692,7 @@ __device__ __forceinline__ void row_warps(const DeltaArgs &a, TcBars &bar, uint3
 
         if (!wait_all(&bar.w_done, c & 1, abort)) return;
         tc_fence_after();
-        uint32_t wb[16], ws[32];
+        uint32_t ws[32];
         tmem_ld32(col_w, ws);
         tmem_ld_wait();
 #pragma unroll
@@ -683,16 +703,13 @@ __device__ __forceinline__ void row_warps(const DeltaArgs &a, TcBars &bar, uint3
                 uint64_t s[2];
                 lds_pairs(vec + (kC + i + j) * 4, s);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t y = ws[i + j + 2 * k], z = ws[i + j + 2 * k + 1];
-                    split2(mul2(s[k], pair_u(y, z)), hi[j / 2 + k], lo[j / 2 + k]);
-                    wb[(i + j) / 2 + k] = pack_bf16x2(f32(y), f32(z));
-                }
+                for (int k = 0; k < 2; ++k)
+                    split2(mul2(s[k], pair_u(ws[i + j + 2 * k], ws[i + j + 2 * k + 1])),
+                           hi[j / 2 + k], lo[j / 2 + k]);
             }
             tmem_st8(t0 + kColOp + half * 16 + i / 2, hi);
             tmem_st8(t0 + kColOp + 32 + half * 16 + i / 2, lo);
         }
-        tmem_st16(t0 + kColX + half * 32, wb);
         tmem_st_wait();
         tc_fence_before();
         arrive_warp(&bar.w_ready);
@@ -733,6 +750,7 @@ __device__ __forceinline__ void issue_products(TcBars &bar, uint32_t base, uint3
     const uint64_t kq0 = smem_desc_sw128(base, 0, 1024);
     const uint64_t kc0 = smem_desc_sw128(base, L::kHalf, 1024);
     const uint64_t tri0 = smem_desc_sw64(base + L::kTris, 512);
+    const uint64_t att0 = smem_desc_sw128(base + L::kTris + kItemAtt, 0, 1024);
 
     auto products_v = [&](int c) {   // V^T, 16 tokens at a time, through the identity
         if (!wait_all(&bar.v_full[c & 1], (c >> 1) & 1, abort)) return false;
@@ -749,6 +767,8 @@ __device__ __forceinline__ void issue_products(TcBars &bar, uint32_t base, uint3
         const int stage = c % kKqStages, buf = c & 1;
         const uint64_t kd = kq0 + stage * (L::kStage >> 4);
         if (!wait_all(&bar.kq_full[stage], (c / kKqStages) & 1, abort)) return;
+        // W of the chunk before, in X's columns, has been read
+        if (c > 0 && !wait_all(&bar.aw_done, (c - 1) & 1, abort)) return;
         if (!wait_all(&bar.s_ready, c & 1, abort)) return;
         tc_fence_after();
         // the parts of S times 16 rows of K (or Q, `rows` bytes behind)
@@ -765,6 +785,7 @@ __device__ __forceinline__ void issue_products(TcBars &bar, uint32_t base, uint3
         if (c > 0 && !wait_all(&bar.o_read, (c - 1) & 1, abort)) return;
         tc_fence_after();
         with_s(Int<0>{}, kColQ, kC * 128, true);
+        with_s(Int<1>{}, kColQ, kC * 128, false);
 
         if (!wait_all(&bar.tri_full[buf], (c >> 1) & 1, abort)) return;
         if (!wait_all(&bar.r_ready, c & 1, abort)) return;
@@ -778,7 +799,7 @@ __device__ __forceinline__ void issue_products(TcBars &bar, uint32_t base, uint3
                                  idesc_bf16_f32(128, 64 - 16 * k, false, false), !first || k > 0);
         };
         const uint64_t tris = tri0 + buf * (HP * kItem >> 4);
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < HP; ++x) {
             if (x >= heads) break;
             const uint32_t d = x ? kColW1 : kColX;
@@ -796,13 +817,23 @@ __device__ __forceinline__ void issue_products(TcBars &bar, uint32_t base, uint3
         for (int k = 0; k < 8; ++k)
             warp_mma_bf16_ts(on, tmem + kColS, tmem + kColOp + k * 8, kc + k % 4 * (2048 >> 4), id_s, k > 0);
         warp_mma_commit(on, &bar.ds_done);
-#pragma unroll
+        warp_mma_commit(on, &bar.kq_empty[stage]);
+        // Att times W, 8 tokens at a time
+#pragma unroll 1   // (a chunk's instructions do not fit the cache otherwise: packed 471 us for 446)
         for (int x = 0; x < HP; ++x) {
             if (x >= heads) break;
-            with_tri(x ? kColW1 : kColAw, kColX, 32,
-                     tris + ((x * kItem + kItemAtt) >> 4), true);
+            if (x) {   // its columns are free
+                if (!wait_all(&bar.ds_done, c & 1, abort)) return;
+                tc_fence_after();
+            }
+            const uint64_t att = att0 + ((buf * HP + x) * kItem >> 4);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                warp_mma_tf32_ts(on, tmem + (x ? kColOp : kColAw) + k / 2 * 16,
+                                 tmem + (x ? kColW1 : kColX) + k * 8,
+                                 att + ((k / 4 * (kAttRight - 32 * 128) + k / 2 * 16 * 128 + k % 4 * 32) >> 4),
+                                 idesc_tf32_f32(128, 64 - k / 2 * 16), k > 0);
         }
-        warp_mma_commit(on, &bar.kq_empty[stage]);
         warp_mma_commit(on, &bar.tri_empty[buf]);
         warp_mma_commit(on, &bar.aw_done);   // last: the CTA's last wait is for it
         if (c + 1 < nchunks && !products_v(c + 1)) return;
