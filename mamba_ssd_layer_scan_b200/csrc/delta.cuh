@@ -120,7 +120,6 @@ struct DeltaBwd {
     float *states;         // (batch, n64 + 1, H, P, N): entering each span; last: the final state
     bf16 *dstates;         // (batch, n64, H, P, N): the gradient of the state leaving each span
     float *wfrag;          // W in accumulator layout, per (batch, chunk, H, tile): 16 x 32
-    bf16 *w;               // (batch, L, H, P): W
     float *dot_oo, *dot_vv, *dot_vw;   // (batch, chunk, H, tile, 32): <dO, O>, <dV, V>, <dV, W>
     float *dot_ss;         // (batch, n64 + 1, H, tile): <dS, S> at the start, then behind each span
     float *dq_part, *dk_part;          // (batch, L, G * runs, N)

@@ -111,7 +111,7 @@ ssd_status check_delta_varlen(const ssd_shape *s, int nseq, const ssd_delta_opti
 
 // The backward's workspace: the items, then what the chains hand to the gradients' kernels.
 struct BwdWs {
-    size_t items, states, dstates, wfrag, w, dot_oo, dot_vv, dot_vw, dot_ss, dq, dk, total;
+    size_t items, states, dstates, wfrag, dot_oo, dot_vv, dot_vw, dot_ss, dq, dk, total;
     int64_t chunks, spans;
     int runs, run_heads;
 };
@@ -149,7 +149,6 @@ BwdWs bwd_ws(const ssd_shape *s)
     w.states = take((spans + (size_t)s->batch * H) * PN * 4);
     w.dstates = take(spans * PN * 2);
     w.wfrag = take(items * (size_t)s->headdim * kDeltaChunk * 4);
-    w.w = take(tokens * H * (size_t)s->headdim * 2);
     w.dot_oo = take(items * tiles * kDeltaChunk * 4);
     w.dot_vv = take(items * tiles * kDeltaChunk * 4);
     w.dot_vw = take(items * tiles * kDeltaChunk * 4);
@@ -354,7 +353,6 @@ ssd_status ssd_delta_rule_bwd(const ssd_shape *shape, const void *q, const void 
     w.states = f32(l.states);
     w.dstates = reinterpret_cast<bf16 *>(ws + l.dstates);
     w.wfrag = f32(l.wfrag);
-    w.w = reinterpret_cast<bf16 *>(ws + l.w);
     w.dot_oo = f32(l.dot_oo);
     w.dot_vv = f32(l.dot_vv);
     w.dot_vw = f32(l.dot_vw);

@@ -34,22 +34,27 @@ constexpr int kSpan = 64;
 constexpr int kGradThreads = 256;
 
 // Tiles of 128- or 256-byte rows, 16-byte piece c of row r at piece c ^ (r % 8): no bank conflicts, and
-// two CTAs to an SM for P = 64.
+// two CTAs to an SM for P = 64.  W and M1 are held in two bf16 parts (rounded to one each they left dq and
+// dk 0.0029 off, 2-norm, for 0.0017 and 0.0020; the rest of the operands does not show beside those); the triangles
+// lie where the states were.
 struct GradSmem {
     static constexpr int mpitch = kSpan * 2;
-    int kpitch, vpitch, k, q, dout, w, dv, s, ds, m1, m2, vec, total;
+    int kpitch, vpitch, k, q, dout, w, wlo, dv, s, ds, m1, m1lo, m2, vec, total;
     __host__ __device__ GradSmem(int P, int N) : kpitch(N * 2), vpitch(P <= 64 ? 128 : 256)
     {
         k = 0;
         q = k + kSpan * kpitch;
         dout = q + kSpan * kpitch;
         w = dout + kSpan * vpitch;
-        dv = w + kSpan * vpitch;
+        wlo = w + kSpan * vpitch;
+        dv = wlo + kSpan * vpitch;
         s = dv + kSpan * vpitch;
         ds = s + P * kpitch;
-        m1 = ds + P * kpitch;
-        m2 = m1 + kSpan * mpitch;
-        vec = m2 + kSpan * mpitch;
+        m1 = s;
+        m1lo = m1 + kSpan * mpitch;
+        m2 = m1lo + kSpan * mpitch;
+        const int states = ds + P * kpitch, triangles = m2 + kSpan * mpitch;
+        vec = states > triangles ? states : triangles;
         total = vec + 8 * kSpan * 4;
     }
 };
@@ -72,7 +77,7 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
     const int g = blockIdx.z / w.runs, run = blockIdx.z % w.runs;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int mt = warp % 4 * 16, nh = warp / 4;   // this warp's 16 tokens and half of the columns
-    const int64_t t0 = span * kSpan, row0 = b * a.L + t0;
+    const int64_t t0 = span * kSpan, row0 = b * a.L + t0, nchunks = (a.L + kDeltaChunk - 1) / kDeltaChunk;
     const int len = (int)(a.L - t0 < kSpan ? a.L - t0 : kSpan);
     const uint32_t base = smem_u32(smem);
     float *vec = reinterpret_cast<float *>(smem + lay.vec);
@@ -130,8 +135,28 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
             const int64_t off = vat + (on ? (int64_t)r * H * P + col * 8 : 0);
             const uint32_t at = swizzled(r, lay.vpitch, col);
             cp16(base + lay.dout + at, w.dout + off, on);
-            cp16(base + lay.w + at, w.w + off, on);
             cp16(base + lay.dv + at, w.dv + off, on);
+        }
+        // W of 16 rows p and 16 tokens at a time, as the chain's accumulators hold it; zeros past the end
+        for (int i = warp; i < P / 4; i += kGradThreads / 32) {
+            const int tile = i / 4, n = i % 4;
+            const int64_t c = span * 2 + n / 2;
+            float4 t[2] = {};
+            if (c < nchunks) {
+                const float *wf = w.wfrag + (((b * nchunks + c) * H + h) * (P / 16) + tile) * (16 * kDeltaChunk);
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+                    t[m] = reinterpret_cast<const float4 *>(wf)[(n % 2 * 2 + m) * 32 + lane];
+            }
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                split2(t[m].x, t[m].y, hi[2 * m], lo[2 * m]);
+                split2(t[m].z, t[m].w, hi[2 * m + 1], lo[2 * m + 1]);
+            }
+            const uint32_t at = swizzled(n * 16 + row_nn, lay.vpitch, tile * 2 + col_nn);
+            stsm4_trans(base + lay.w + at, hi);
+            stsm4_trans(base + lay.wlo + at, lo);
         }
         const bf16 *dsg = w.dstates + ((b * w.n64 + span) * H + h) * P * N;
         for (int i = tid; i < P * (N / 8); i += kGradThreads)
@@ -194,6 +219,41 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
         cp_wait<0>();
         __syncthreads();
 
+        // products with the states, then scaled row by row: x, y = tiles of rows (dO, dV, or W's two parts)
+        auto with_state = [&](uint32_t x, uint32_t y, uint32_t st, const float *f, float sign,
+                              float (&to)[NT][4]) {
+            float acc[NT][4] = {};
+            for (int s = 0; s < P / 16; ++s) {
+                uint32_t fa[4], fl[4], fb[4];
+                const uint32_t at = swizzled(mt + row_a, lay.vpitch, s * 2 + col_a);
+                ldsm4(fa, base + x + at);
+                if (y) ldsm4(fl, base + y + at);
+#pragma unroll
+                for (int n = 0; n < NT / 2; ++n) {
+                    ldsm4_trans(fb, base + st + swizzled(s * 16 + row_kk, lay.kpitch,
+                                                         nh * N / 16 + n * 2 + col_kk));
+                    mma_16816(acc[2 * n], fa, fb[0], fb[1]);
+                    mma_16816(acc[2 * n + 1], fa, fb[2], fb[3]);
+                    if (y) {
+                        mma_16816(acc[2 * n], fl, fb[0], fb[1]);
+                        mma_16816(acc[2 * n + 1], fl, fb[2], fb[3]);
+                    }
+                }
+            }
+            const float f0 = sign * f[mt + lane / 4], f1 = sign * f[mt + lane / 4 + 8];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                to[n][0] = fmaf(f0, acc[n][0], to[n][0]);
+                to[n][1] = fmaf(f0, acc[n][1], to[n][1]);
+                to[n][2] = fmaf(f1, acc[n][2], to[n][2]);
+                to[n][3] = fmaf(f1, acc[n][3], to[n][3]);
+            }
+        };
+        with_state(lay.dout, 0, lay.s, eq, 1.f, dq);
+        with_state(lay.w, lay.wlo, lay.ds, sw, 1.f, dk);
+        with_state(lay.dv, 0, lay.s, ek, -1.f, dk);
+        __syncthreads();   // the states' place is the triangles' now
+
         {   // M1 (warps 0-3) and M2 (warps 4-7): 16 rows, the columns up to the diagonal
             const uint32_t rows = base + (nh ? lay.dv : lay.dout);
             const uint32_t out = nh ? lay.m2 : lay.m1;
@@ -205,7 +265,11 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     if (n * 16 > mt) break;
-                    ldsm4(fb, base + lay.w + swizzled(n * 16 + row_nn, lay.vpitch, s * 2 + col_nn));
+                    const uint32_t at = swizzled(n * 16 + row_nn, lay.vpitch, s * 2 + col_nn);
+                    ldsm4(fb, base + lay.w + at);
+                    mma_16816(acc[2 * n], fa, fb[0], fb[1]);
+                    mma_16816(acc[2 * n + 1], fa, fb[2], fb[3]);
+                    ldsm4(fb, base + lay.wlo + at);
                     mma_16816(acc[2 * n], fa, fb[0], fb[1]);
                     mma_16816(acc[2 * n + 1], fa, fb[2], fb[3]);
                 }
@@ -221,40 +285,15 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
                     const float d0 = (ci - cs[j]) + (li - cl[j]), d1 = (ci - cs[j + 1]) + (li - cl[j + 1]);
                     const float x = on0 ? acc[n][2 * r] * f * __expf(d0) * kb[j] : 0.f;
                     const float y = on1 ? acc[n][2 * r + 1] * f * __expf(d1) * kb[j + 1] : 0.f;
-                    *reinterpret_cast<uint32_t *>(smem + out + swizzled(i, lay.mpitch, n) + j % 8 * 2) =
-                        pack_bf16x2(x, y);
+                    const uint32_t at = swizzled(i, lay.mpitch, n) + j % 8 * 2;
+                    uint32_t hi, lo;
+                    split2(x, y, hi, lo);
+                    *reinterpret_cast<uint32_t *>(smem + out + at) = hi;
+                    if (!nh) *reinterpret_cast<uint32_t *>(smem + lay.m1lo + at) = lo;
                 }
             }
         }
         __syncthreads();
-
-        // products with the states, then scaled row by row: x = tile rows (dO, W or dV)
-        auto with_state = [&](uint32_t x, uint32_t st, const float *f, float sign,
-                              float (&to)[NT][4]) {
-            float acc[NT][4] = {};
-            for (int s = 0; s < P / 16; ++s) {
-                uint32_t fa[4], fb[4];
-                ldsm4(fa, base + x + swizzled(mt + row_a, lay.vpitch, s * 2 + col_a));
-#pragma unroll
-                for (int n = 0; n < NT / 2; ++n) {
-                    ldsm4_trans(fb, base + st + swizzled(s * 16 + row_kk, lay.kpitch,
-                                                         nh * N / 16 + n * 2 + col_kk));
-                    mma_16816(acc[2 * n], fa, fb[0], fb[1]);
-                    mma_16816(acc[2 * n + 1], fa, fb[2], fb[3]);
-                }
-            }
-            const float f0 = sign * f[mt + lane / 4], f1 = sign * f[mt + lane / 4 + 8];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                to[n][0] = fmaf(f0, acc[n][0], to[n][0]);
-                to[n][1] = fmaf(f0, acc[n][1], to[n][1]);
-                to[n][2] = fmaf(f1, acc[n][2], to[n][2]);
-                to[n][3] = fmaf(f1, acc[n][3], to[n][3]);
-            }
-        };
-        with_state(lay.dout, lay.s, eq, 1.f, dq);
-        with_state(lay.w, lay.ds, sw, 1.f, dk);
-        with_state(lay.dv, lay.s, ek, -1.f, dk);
 
         // products with the triangles; K's and Q's columns as B operands
         auto with_rows = [&](const uint32_t (&fa)[4], uint32_t rows, int s, float (&to)[NT][4]) {
@@ -270,17 +309,23 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
         for (int s = 0; s < 4; ++s) {
             uint32_t fa[4];
             if (s * 16 <= mt) {   // tokens up to these
-                ldsm4(fa, base + lay.m1 + swizzled(mt + row_a, lay.mpitch, s * 2 + col_a));
+                const uint32_t at = swizzled(mt + row_a, lay.mpitch, s * 2 + col_a);
+                ldsm4(fa, base + lay.m1 + at);
                 with_rows(fa, lay.k, s, dq);
-                ldsm4(fa, base + lay.m2 + swizzled(mt + row_a, lay.mpitch, s * 2 + col_a));
+                ldsm4(fa, base + lay.m1lo + at);
+                with_rows(fa, lay.k, s, dq);
+                ldsm4(fa, base + lay.m2 + at);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) fa[r] ^= 0x80008000u;
                 with_rows(fa, lay.k, s, dk);
             }
             if (s * 16 >= mt) {   // tokens from these on: transposed
-                ldsm4_trans(fa, base + lay.m1 + swizzled(s * 16 + row_nn, lay.mpitch, mt / 8 + col_nn));
+                const uint32_t at = swizzled(s * 16 + row_nn, lay.mpitch, mt / 8 + col_nn);
+                ldsm4_trans(fa, base + lay.m1 + at);
                 with_rows(fa, lay.q, s, dk);
-                ldsm4_trans(fa, base + lay.m2 + swizzled(s * 16 + row_nn, lay.mpitch, mt / 8 + col_nn));
+                ldsm4_trans(fa, base + lay.m1lo + at);
+                with_rows(fa, lay.q, s, dk);
+                ldsm4_trans(fa, base + lay.m2 + at);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) fa[r] ^= 0x80008000u;
                 with_rows(fa, lay.k, s, dk);

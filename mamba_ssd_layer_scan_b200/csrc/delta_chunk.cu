@@ -517,10 +517,6 @@ delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64
                     }
                 }
         }
-        int64_t t0;
-        int len;
-        chunk_span(tab, c, C, a.L, t0, len);
-        const int64_t tokens = ((b * a.L + t0) * a.H + h) * P + p0;   // this warp's rows of v, o
         if constexpr (kBwd) {
             float d[8];   // <dO, O> over this warp's rows, per token
 #pragma unroll
@@ -542,8 +538,6 @@ delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64
 #pragma unroll
             for (int t = 0; t < 4; ++t)
                 wf[t * 32] = make_float4(W[t][0], W[t][1], W[t][2], W[t][3]);
-            store_tokens(W, vs + pl * 2, lay.vpitch, vaddr, w.w + tokens, (int64_t)a.H * P, len,
-                         lane);
         }
         // S = E S + (E / e beta W)^T K
         const float E = vec[3 * C];
@@ -575,9 +569,14 @@ delta_chain_kernel(const DeltaArgs a, const DeltaBwd w, const char *items, int64
                 }
             }
         }
-        if constexpr (!kBwd)
-            store_tokens(O, vs + pl * 2, lay.vpitch, vaddr, static_cast<bf16 *>(a.o) + tokens,
+        if constexpr (!kBwd) {
+            int64_t t0;
+            int len;
+            chunk_span(tab, c, C, a.L, t0, len);
+            store_tokens(O, vs + pl * 2, lay.vpitch, vaddr,
+                         static_cast<bf16 *>(a.o) + ((b * a.L + t0) * a.H + h) * P + p0,
                          (int64_t)a.H * P, len, lane);
+        }
     }
     __syncthreads();   // the load warps' last one
     let_next_start();

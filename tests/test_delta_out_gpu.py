@@ -54,3 +54,39 @@ def test_packed(cuda_device, P, H):
         init_states=d["init"].to(cuda_device), qk_l2norm=True)
     assert o.numel() >= 75000
     assert ref.rel(o, torch.cat(parts, 1)) <= bound(cu[-1])
+
+
+@pytest.mark.parametrize("b,L,H,G,P,N", [(8, 60, 6, 2, 64, 128), (8, 64, 4, 2, 128, 64),
+                                         (12, 33, 4, 4, 48, 64), (6, 50, 9, 1, 128, 128)])
+def test_gradients_of_keys_and_queries_are_off_by_their_rounding(cuda_device, b, L, H, G, P, N):
+    """Within one span of 64 tokens from an empty state, with no gradient of the final one, dq is sum over
+    j <= i of M1_ij k_j, M1_ij = scale exp(cs_i - cs_j) beta_j (dO_i . W_j): neither M1 nor W is rounded to
+    bf16 as a whole, and dq is off by its own rounding.  dk is M1^T q less (M2 + M2^T) k, M2_ij = exp(cs_i -
+    cs_j) beta_j (dV_i . W_j) below the diagonal, where M2 and dV are rounded: 2^-8 / sqrt(3) of that term
+    each."""
+    d = ref.draw(b, L, H, G, P, N, BF, seed=L + P, init=False)
+    dout = torch.randn((b, L, H, P), generator=torch.Generator().manual_seed(3)).to(BF)
+    leaf = {n: d[n].double().requires_grad_() for n in ("q", "k", "v", "g", "beta")}
+    o, _ = ref.delta_rule(*leaf.values(), None, N ** -0.5, False)
+    o.backward(dout.double())
+    # W by the recurrence, then the term of M2
+    k, v, g, beta = (leaf[n].detach() for n in ("k", "v", "g", "beta"))
+    k = ref.heads(k, H)
+    S, W = torch.zeros(b, H, P, N, dtype=torch.float64), []
+    for t in range(L):
+        S = torch.exp(g[:, t])[..., None, None] * S
+        W.append(v[:, t] - (S * k[:, t, :, None, :]).sum(-1))
+        S = S + (beta[:, t, :, None] * W[-1])[..., None] * k[:, t, :, None, :]
+    W = torch.stack(W, 1)
+    cs = g.cumsum(1)
+    M2 = torch.einsum("bihp,bjhp->bhij", leaf["v"].grad, W) * beta.transpose(1, 2)[:, :, None]
+    M2 = (M2 * torch.exp((cs[:, :, None] - cs[:, None]).permute(0, 3, 1, 2).clamp(max=0))).tril(-1)
+    term = torch.einsum("bhij,bjhn->bihn", M2 + M2.transpose(2, 3), k)
+    term = term.unflatten(2, (G, -1)).sum(3)
+    got = ssd.delta_rule_bwd(*(d[n].to(cuda_device) for n in ("q", "k", "v", "g", "beta")),
+                             dout.to(cuda_device))
+    u, more = 1.02 * 2.0 ** -8 / 3 ** 0.5, 8 * 2.0 ** -16 + 8 * (L + 32) * 2.0 ** -24
+    dq, dk = leaf["q"].grad, leaf["k"].grad
+    assert ref.rel(got["dq"], dq) <= u + more
+    share = float(term.norm() / dk.norm())
+    assert ref.rel(got["dk"], dk) <= u * (1 + 2 * share ** 2) ** 0.5 + more
