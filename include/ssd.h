@@ -362,9 +362,9 @@ ssd_status ssd_chunk_scan_fwd_static_status(void *stream);
  * q, k, v, o and the states must be 16-byte aligned.  batch == 0 or seqlen == 0 is valid.
  *
  * bf16 with dstate 64 or 128 and headdim a multiple of 16 runs in chunks of 32 or 64 tokens, on
- * tcgen05 for headdim 64 and 128 once there is enough to do; the state keeps float32's usual
- * accuracy.  A NaN or infinity at a token reaches, in its own sequence and head (a key's or query's:
- * its group's heads), the later tokens and the outputs of its chunk.
+ * tcgen05 for headdim 64 and 128 once there is enough to do: o is then off by its own rounding (0.0017,
+ * 2-norm), final states by 3e-6.  A NaN or infinity at a token reaches, in its own sequence and head (a
+ * key's or query's: its group's heads), the later tokens and the outputs of its chunk.
  */
 typedef struct {
     float scale;          /* of the output; usually 1 / sqrt(dstate) */
@@ -408,7 +408,8 @@ ssd_status ssd_delta_rule_varlen_fwd(const ssd_shape *shape, const void *q, cons
  *   dq, dk, dv   like q, k and v, in their type;  dg, dbeta (batch, seqlen, nheads) float32, dg
  *                with g (NULL where g is);  dinit (batch, nheads, headdim, dstate) float32,
  *                nullable.  No output may alias an input.  A beta nearer to 0 than 1e-20 is taken
- *                as 1e-20.  Repeated calls give the same bits.
+ *                as 1e-20.  Repeated calls give the same bits.  dv is off by its own rounding (0.0017,
+ *                2-norm), dq by 0.0018, dk by 0.0019, dg, dbeta and dinit by 3e-6 to 4e-6.
  *   workspace    ssd_delta_rule_bwd_workspace_size bytes (0: invalid or unsupported), 256-byte
  *                aligned.
  * bf16, headdim a multiple of 16 and dstate 64 or 128; other shapes return SSD_ERR_UNSUPPORTED.

@@ -8,10 +8,10 @@ namespace {
 
 // The kernels of a forward pass.  Below kChunkTokens the token recurrence, one launch, is as fast as
 // the chunked kernels.  Of these the warp-level ones (16 state rows to a warp) are ahead while each
-// warp has an SM to itself, by 5 us at any length (8 heads of 64, N 128, us: 129 tokens 16 against
-// 21, 2048 tokens 94 against 103; 37 heads 17 against 21, 105 against 109), and for sequences of up
-// to 64 tokens (8 x 80 heads: 34 against 38; of 128 tokens 55 against 48); with more to do the
-// tcgen05 ones are (80 heads, 2048 tokens: 125 against 182; 8 x 80 heads 442 against 643).
+// warp has an SM to itself, by 6 us for short sequences and as fast for long ones (8 heads of 64, N 128,
+// us: 129 tokens 18 against 25, 2048 tokens 104 against 105; 37 heads 19 against 25, 115 against 113), and
+// for sequences of up to 64 tokens (8 x 80 heads: 37 against 47; of 128 tokens 61 against 62); with more
+// to do the tcgen05 ones are (80 heads, 2048 tokens: 131 against 209; 8 x 80 heads 456 against 699).
 constexpr int kChunkTokens = 24, kTcTokens = 64;
 constexpr int64_t kTcRows = 148 * 16;
 

@@ -18,10 +18,10 @@
 //     dg_t = <dS', S'> + sum over s >= t of x_s = <dS, S> - sum over s < t of x_s
 //     dbeta_t = <dV_t, W_t> / beta_t
 //
-// where the dot products come from the chains in float32 (the gradients' kernel takes 78 us at 2 x 2048
-// tokens x 24 heads, latency of a head's loads and barriers; with one CTA to an SM 108).  The errors of the two sums add up over
-// n - t and t terms that partly cancel; weighted by t / n and (n - t) / n they give 0.6 of the first
-// one's error alone (7e-6 for 1.2e-5 of dg, 2-norm, at 2 x 2048 x 24 heads).
+// where the dot products come from the chains in float32 (the gradients' kernel takes 97 us at 2 x 2048
+// tokens x 24 heads, latency of a head's loads and barriers, with two CTAs to an SM).  The errors of the two
+// sums add up over n - t and t terms that partly cancel; weighted by t / n and (n - t) / n they give 0.6 of
+// the first one's error alone (dg at 2 x 2048 x 24 heads: 4e-6, 2-norm).
 #include "delta.cuh"
 #include "delta_mma.cuh"
 
@@ -34,9 +34,9 @@ constexpr int kSpan = 64;
 constexpr int kGradThreads = 256;
 
 // Tiles of 128- or 256-byte rows, 16-byte piece c of row r at piece c ^ (r % 8): no bank conflicts, and
-// two CTAs to an SM for P = 64.  W and M1 are held in two bf16 parts (rounded to one each they left dq and
-// dk 0.0029 off, 2-norm, for 0.0017 and 0.0020; the rest of the operands does not show beside those); the triangles
-// lie where the states were.
+// two CTAs to an SM for P = 64.  W and M1 are held in two bf16 parts: rounded to one they left dq and dk
+// 0.0029 off (2-norm) where their own rounding is 0.0017; now 0.0017 and 0.0019, what dS, S, dV and M2,
+// rounded to bf16, add.  The triangles lie where the states were.
 struct GradSmem {
     static constexpr int mpitch = kSpan * 2;
     int kpitch, vpitch, k, q, dout, w, wlo, dv, s, ds, m1, m1lo, m2, vec, total;
@@ -143,7 +143,8 @@ delta_grad_kernel(const DeltaArgs a, const DeltaBwd w)
             const int64_t c = span * 2 + n / 2;
             float4 t[2] = {};
             if (c < nchunks) {
-                const float *wf = w.wfrag + (((b * nchunks + c) * H + h) * (P / 16) + tile) * (16 * kDeltaChunk);
+                const float *wf = w.wfrag + (((b * nchunks + c) * H + h) * (P / 16) + tile) *
+                                                (16 * kDeltaChunk);
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
                     t[m] = reinterpret_cast<const float4 *>(wf)[(n % 2 * 2 + m) * 32 + lane];

@@ -23,12 +23,13 @@
 // The backward's dg is a small difference of these products: what two parts leave of the values that
 // are written, of dS in dS K^T and of W in Att W came to 1e-5 and more of dg for one call in eighty of a
 // few tokens and heads (2.7e-5 at worst of 1800 such calls).  There these take three parts, and that is
-// 6e-6 at worst; 44 and 32 matrix instructions more in the two chains, 413 -> 451 us at 2 x 2048 x 24 heads.
+// 7e-6 at worst; 44 and 32 matrix instructions more in the two chains, about 30 us of 445 at 2 x 2048 x 24
+// heads.
 //
 // Bound: with many heads the rate of the warp-level matrix instructions (one m16n8k16 in 8 cycles per
 // SM quarter), where the tcgen05 form takes over; with few, where a warp has its SM quarter to itself,
-// the latency of its chain, 1.35 us a chunk: 129 tokens x 8 heads 16 us, 2048 tokens x 8 heads 94 us.
-// The backward's chains at 2 x 2048 x 24 heads: 146 and 162 us.
+// the latency of its chain, 1.5 us a chunk: 129 tokens x 8 heads 18 us, 2048 tokens x 8 heads 104 us.
+// The backward's chains at 2 x 2048 x 24 heads: 142 and 178 us.
 #include "delta.cuh"
 #include "delta_mma.cuh"
 
@@ -223,7 +224,7 @@ struct ChainStage {
     static __host__ __device__ constexpr int state_pitch(int N) { return N * 4 + 32; }
 };
 // The adjoint chain reads the states and W through its stage where a CTA has one warp of rows, bound by
-// what a chunk waits for (2 x 2048 tokens x 24 heads: 183 -> 162 us); with more rows the space is
+// what a chunk waits for (2 x 2048 tokens x 24 heads, dS in two parts: 183 -> 162 us); with more rows the space is
 // worth more as a second CTA on the SM.
 __host__ __device__ constexpr bool adjoint_staged(int rows) { return rows == 16; }
 

@@ -13,13 +13,13 @@
 // output alone, is a product of float32 operands cut to 10 bits, W read where its product left it.  (Of
 // bf16 operands it was off by as much as the output's own rounding for each of the two, 0.0033 for 0.0017
 // in all; in two bf16 parts each it took half as much again and the parts' making: packed 16384 tokens x
-// 80 heads 487 us, this form 446, bf16 420.)  The state itself stays in registers, float32.  Two heads that share a
-// CTA multiply all 128 rows by each head's triangles and read their own result: 2 x 64 columns
-// cost the same as a block-diagonal product, and what is not finite in one head stays there.
+// 80 heads 487 us, this form 446, bf16 420.)  The state itself stays in registers, float32.  Two heads
+// that share a CTA multiply all 128 rows by each head's triangles and read their own result: 2 x 64
+// columns cost the same as a block-diagonal product, and what is not finite in one head stays there.
 //
 // Bound: the chain of a chunk, three products deep (500-700 cycles each) with the rows' splits and the
-// hand-overs between them, 5400 cycles: 2 x 4096 tokens x 32 heads of 128 take 180 us, 64 chunks of 2.8 us,
-// behind 50 us for the triangles; 16384 packed tokens x 80 heads of 64 250 us behind 150 us.  64 tokens
+// hand-overs between them, 5400 cycles: 2 x 4096 tokens x 32 heads of 128 take 179 us, 64 chunks of 2.8 us,
+// behind 60 us for the triangles; 16384 packed tokens x 80 heads of 64 270 us behind 158 us.  64 tokens
 // to a chunk: of 32 the same products would have half the columns, and the hand-overs twice their share.
 #include "delta.cuh"
 #include "delta_mma.cuh"
@@ -42,8 +42,9 @@ template <int I> struct Int { static constexpr int value = I; };
 
 // ---------------------------------------------------------------- the triangles
 // A triangle, 64 x 64 bf16 in 6 KB: columns 0-31 of all rows, then columns 32-63 of rows 32-63, in
-// rows of 64 bytes, 64-byte swizzled; in float32 (Att) 12 KB, in rows of 128 bytes, 128-byte swizzled.  An item, per chunk and head: Inv in two parts, Att,
-// and the factors -ek, sw, eq (64 floats each) and E (four times).
+// rows of 64 bytes, 64-byte swizzled; in float32 (Att) 12 KB, in rows of 128 bytes, 128-byte swizzled.
+// An item, per chunk and head: Inv in two parts, Att, and the factors -ek, sw, eq (64 floats each) and E
+// (four times).
 constexpr int kMat = 6 * 1024, kMatRight = 4 * 1024, kAttRight = 8 * 1024;
 constexpr int kMats = 4 * kMat, kItemAtt = 2 * kMat, kItemVec = kMats, kVecFloats = 3 * kC + 4;
 constexpr int kItem = kDeltaTcItem, kItemUsed = kItemVec + kVecFloats * 4;

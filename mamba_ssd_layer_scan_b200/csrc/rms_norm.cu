@@ -13,8 +13,12 @@
 // row's largest |h w| (forward, one scale per row) or with sum(dn w h) (backward) -- and written.
 // A row of up to 32 vectors belongs to 8, 16 or 32 lanes of a warp, a longer one to a whole CTA;
 // the CTAs walk the rows with their slice of w in registers and the next rows on their way.
-// Measured (bf16): 16384 x 2560 with a residual 60 us, 85 % of the copy bandwidth, its backward 68 + 4 us;
-// 8191 x 5120 gated, e4m3 by groups of 128, 50 us (64 %, issue slots); 98304 x 64 gated backward 17 + 4 us.
+// Measured (bf16): 16384 x 2560 with a residual 64 us, 80 % of the copy bandwidth, its backward 73 us;
+// 8191 x 5120 gated, e4m3 by groups of 128, 50 us (65 %, issue slots); 98304 x 64 gated backward 20.5 us.
+// The backward of rows above 8192 values holds weights, their gradients and up to three operands in
+// registers that do not suffice (0.2 to 2 KB a thread go to local memory; value by value above 4096
+// already): 8192 rows of 16384 run at 60 to 79 % of the copy bandwidth, gated 48 to 53 %, of 16383 at 18 %,
+// gated 20 %.
 #include <algorithm>
 #include <atomic>
 
